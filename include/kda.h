@@ -367,6 +367,208 @@ KDA_API int kda_output_correct(const void* C, const float* S_in, const void* o_i
                                int dk, int dv, int dtype, struct CUstream_st* stream);
 
 /*
+ * ---------------------------------------------------------------------------------------------
+ * The short causal convolution, the selective scan and the state pools: what a serving engine runs
+ * beside the KDA recurrence.  Conventions as above, with one difference: the activations may be
+ * slices of wider rows.  Each `ld*` argument is the distance in elements from one token's row to the
+ * next (the row itself is contiguous), so that the q, k, v or x, B, C parts of one projection are
+ * passed without a copy; batch entry b starts at row b*T.  Rows of vector-loaded tensors (x, y, Bm,
+ * Cm) start on 16-byte boundaries: their ld is a multiple of 16 bytes.  dt, A, D and dt_bias need
+ * their element's alignment only.  Inputs and outputs are compared by the whole range from their
+ * first to their last byte: an output may not lie between the rows of an input.
+ */
+
+/* Activation of the short convolution. */
+typedef enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 } kda_activation;
+
+/*
+ * kda_short_conv -- the depthwise causal convolution of width W before the recurrence (each of its
+ * inputs q, k, v, or x, B, C of the selective scan, is such a convolution of its projection):
+ *
+ *   y[b,t,c] = act( bias[c] + sum_{w < W} weight[c,w] u[b, t-(W-1)+w, c] )
+ *
+ * where u is the sequence x[b] preceded by its last W-1 inputs, `state`.  fp32 arithmetic.
+ *
+ *   x         : [B, T, C]     dtype, row stride ldx >= C
+ *   weight    : [C, W]        dtype (a depthwise kernel as frameworks keep it)
+ *   bias      : [C]           dtype, or NULL for none
+ *   state     : [B, W-1, C]   dtype, the inputs before token 0 (oldest first), or NULL for zeros
+ *   y         : [B, T, C]     dtype output, row stride ldy >= C
+ *   state_out : [B, W-1, C]   dtype output, the last W-1 inputs (of `state` too when T < W-1), or NULL.
+ *               May be `state` itself; no other overlap between outputs and inputs.
+ *   W         : 2, 3 or 4.  C: a positive multiple of 8.
+ *
+ * T == 0 copies state to state_out.  Returns KDA_OK; KDA_ERR_UNSUPPORTED for another W, a C that is
+ * not a multiple of 8, another dtype or activation.
+ */
+KDA_API int kda_short_conv(const void* x, const void* weight, const void* bias, const void* state, void* y,
+                           void* state_out, int B, int T, int C, int W, long long ldx, long long ldy,
+                           int activation, int dtype, struct CUstream_st* stream);
+
+/*
+ * kda_short_conv_varlen -- kda_short_conv over N sequences packed along the token axis.
+ *
+ *   x, y             : [T_total, C]; cu_seqlens : [N + 1] int32 DEVICE array, rules of kda_forward_varlen
+ *                      (checked by the kernel: offsets that break them leave every sequence empty and
+ *                      set the status word).  y rows outside every sequence are not written.
+ *   state, state_out : [N, W-1, C]
+ */
+KDA_API int kda_short_conv_varlen(const void* x, const void* weight, const void* bias, const int* cu_seqlens,
+                                  const void* state, void* y, void* state_out, int N, int T_total, int C, int W,
+                                  long long ldx, long long ldy, int activation, int dtype,
+                                  struct CUstream_st* stream);
+
+/*
+ * kda_short_conv_step -- one token for every sequence; `state` [B, W-1, C] is shifted in place.
+ *   x, y : [B, C], row strides ldx, ldy.
+ */
+KDA_API int kda_short_conv_step(const void* x, const void* weight, const void* bias, void* state, void* y, int B,
+                                int C, int W, long long ldx, long long ldy, int activation, int dtype,
+                                struct CUstream_st* stream);
+
+/*
+ * kda_short_conv_step_paged -- kda_short_conv_step with the states in a pool [n_slots, W-1, C]:
+ * sequence b uses slots[b]; rules of kda_decode_step_paged (negative: skipped, y[b] untouched; a slot
+ * >= n_slots is skipped and sets the status word; active slots are distinct).
+ */
+KDA_API int kda_short_conv_step_paged(const void* x, const void* weight, const void* bias, void* state_pool,
+                                      int n_slots, const int* slots, void* y, int B, int C, int W, long long ldx,
+                                      long long ldy, int activation, int dtype, struct CUstream_st* stream);
+
+/*
+ * kda_ssm_forward -- prefill of the selective state space scan with one decay per head:
+ *
+ *   s_t = softplus(dt_t + dt_bias)                      (per token and head)
+ *   S_t = exp(s_t A) S_{t-1} + B_t (s_t x_t)^T          (S in R^{N x P}, fp32)
+ *   y_t = S_t^T C_t + D x_t
+ *
+ * i.e. the recurrence of kda_forward_chunked with a scalar decay and no delta rule: B, C, x stand in
+ * the places of k, q, v.  The H heads share G pairs (B, C): head h uses pair h / (H / G).
+ *
+ *   x       : [B, T, H, P]  dtype, token stride ldx >= H*P
+ *   dt      : [B, T, H]     dtype, token stride lddt >= H
+ *   A       : [H]           fp32 (A <= 0: a decay)
+ *   Bm, Cm  : [B, T, G, N]  dtype, token strides ldb, ldc >= G*N
+ *   D       : [H]           fp32, or NULL for no skip term
+ *   dt_bias : [H]           fp32, or NULL for zero
+ *   S0      : [B, H, N, P]  fp32, or NULL for zero
+ *   y       : [B, T, H, P]  dtype output, contiguous
+ *   S_T     : [B, H, N, P]  fp32 output, or NULL; may be S0 itself; no other overlap
+ *   N, P    : 64 or 128.  G divides H.
+ *   impl    : kda_impl.  KDA_IMPL_AUTO and KDA_IMPL_SIMT run the token-serial fp32 kernel;
+ *             KDA_IMPL_TCGEN05 is refused.
+ *   workspace, workspace_bytes : DEVICE memory of at least kda_ssm_workspace(...) bytes, 16-byte
+ *             aligned (NULL when that is 0), not used by anything else until the work is done.
+ *
+ * T == 0 copies S0 to S_T.
+ */
+KDA_API int kda_ssm_forward(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
+                            const float* D, const float* dt_bias, const float* S0, void* y, float* S_T, int B,
+                            int T, int H, int G, int N, int P, long long ldx, long long lddt, long long ldb,
+                            long long ldc, int dtype, int impl, void* workspace, size_t workspace_bytes,
+                            struct CUstream_st* stream);
+
+/*
+ * kda_ssm_forward_varlen -- kda_ssm_forward over n_seq sequences packed along the token axis.
+ *
+ *   x, dt, Bm, Cm, y : [T_total, ...]; cu_seqlens : [n_seq + 1] int32 DEVICE array, rules of
+ *                      kda_forward_varlen.  y rows outside every sequence are not written.
+ *   S0, S_T          : [n_seq, H, N, P]
+ */
+KDA_API int kda_ssm_forward_varlen(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
+                                   const int* cu_seqlens, const float* D, const float* dt_bias, const float* S0,
+                                   void* y, float* S_T, int n_seq, int T_total, int H, int G, int N, int P,
+                                   long long ldx, long long lddt, long long ldb, long long ldc, int dtype, int impl,
+                                   void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
+
+/*
+ * kda_ssm_workspace -- bytes of device workspace kda_ssm_forward (n_seq = B, T_total = B*T) or
+ * kda_ssm_forward_varlen needs.  0 where none is needed (and for sizes the calls refuse).
+ */
+KDA_API size_t kda_ssm_workspace(int n_seq, int T_total, int H, int N, int P, int dtype, int impl);
+
+/*
+ * kda_ssm_decode_step -- one token for every (b, h), S [B, H, N, P] updated in place.
+ *   x, y : [B, H, P] (x with row stride ldx, y contiguous); dt : [B, H]; Bm, Cm : [B, G, N].
+ */
+KDA_API int kda_ssm_decode_step(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
+                                const float* D, const float* dt_bias, float* S, void* y, int B, int H, int G, int N,
+                                int P, long long ldx, long long lddt, long long ldb, long long ldc, int dtype,
+                                struct CUstream_st* stream);
+
+/*
+ * kda_ssm_decode_step_paged -- kda_ssm_decode_step with the states in a pool [n_slots, H, N, P]:
+ * sequence b uses slots[b]; rules of kda_decode_step_paged.
+ */
+KDA_API int kda_ssm_decode_step_paged(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
+                                      const float* D, const float* dt_bias, float* S_pool, int n_slots,
+                                      const int* slots, void* y, int B, int H, int G, int N, int P, long long ldx,
+                                      long long lddt, long long ldb, long long ldc, int dtype,
+                                      struct CUstream_st* stream);
+
+/*
+ * kda_pool -- one state pool as the pool operators see it: n_slots slots of `pieces` runs of
+ * piece_bytes each.  A pool [n_slots, H, dk, dv] is one piece a slot; the boundary states of one batch
+ * entry, S_mid[b] of kda_forward_chunked_states ([H, n_mid, dk, dv], slot = boundary), are H pieces.
+ * All byte counts and the base are multiples of 16.
+ */
+typedef struct {
+    void* base;
+    long long slot_stride;  /* bytes from one slot to the next */
+    long long pieces;       /* runs of contiguous bytes in a slot */
+    long long piece_stride; /* bytes from one run of a slot to the next */
+    long long piece_bytes;  /* bytes of one run */
+} kda_pool;
+
+/*
+ * kda_pool_copy -- copy slots, in every pool at once: slot dst_idx[i] of dst[p] becomes slot
+ * src_idx[i] of src[p], for i < n and p < n_pools (all layers of a model in one call).  One source may
+ * feed many destinations (forking a sequence).
+ *
+ *   dst, src         : HOST arrays of n_pools pools; dst[p] and src[p] have the same pieces and
+ *                      piece_bytes, and are the same pool or do not overlap
+ *   n_dst, n_src     : slots of every dst and every src pool
+ *   src_idx, dst_idx : [n] int32 DEVICE arrays; a pair with a negative index is skipped
+ *
+ * A pair is not copied, and the status word is set to KDA_ERR_INVALID_ARG, when an index is past its
+ * pool, when another pair has the same destination, or when (dst[p] being src[p]) its destination is
+ * the source of another pair: the result never depends on the order of the copies.  A pair of a slot
+ * with itself does nothing.
+ */
+KDA_API int kda_pool_copy(const kda_pool* dst, const kda_pool* src, int n_pools, int n_dst, int n_src,
+                          const int* src_idx, const int* dst_idx, int n, struct CUstream_st* stream);
+
+/*
+ * kda_pool_clear -- set slots to zero bytes in every pool: the state a new sequence starts from.
+ *   idx : [n] int32 DEVICE array; negative entries are skipped, entries >= n_slots are skipped and set
+ *         the status word.
+ */
+KDA_API int kda_pool_clear(const kda_pool* pools, int n_pools, int n_slots, const int* idx, int n,
+                           struct CUstream_st* stream);
+
+/*
+ * kda_pool_compact -- drop the sequences that ended and move the live ones' states to the front.
+ *
+ * Sequence b is live if slots[b] >= 0 and done[b] == 0.  With L live sequences, the live slots >= L, in
+ * ascending order, move into the slots < L that are not live, in ascending order, in every pool; the
+ * other slots keep their contents.
+ *
+ *   slots     : [B] int32 DEVICE array, the table of kda_decode_step_paged
+ *   done      : [B] bytes (0 or not) in DEVICE memory, or NULL for none ended
+ *   slots_out : [B] int32 DEVICE output: the new table, -1 for sequences that are not live.  May be
+ *               slots itself.
+ *   workspace : DEVICE int32 array of n_slots + 1 entries (16-byte aligned) that nothing else uses until
+ *               the work is done; entry 0 receives the number of slots moved.
+ *   n_slots   : at most 65536 (KDA_ERR_UNSUPPORTED above)
+ *
+ * Two live sequences on one slot, or a live slot >= n_slots, set the status word to
+ * KDA_ERR_INVALID_ARG; then nothing moves and slots_out is slots.
+ */
+KDA_API int kda_pool_compact(const kda_pool* pools, int n_pools, int n_slots, const int* slots,
+                             const unsigned char* done, int* slots_out, int B, int* workspace,
+                             struct CUstream_st* stream);
+
+/*
  * kda_get_device_status -- synchronise `stream`, then return and clear the status word
  * of the current device: KDA_OK, KDA_ERR_TIMEOUT (a kernel's bounded wait gave up; its
  * outputs are then undefined), KDA_ERR_INVALID_ARG (a kernel found an out-of-range device

@@ -10,12 +10,17 @@ these functions raise.
     o, S_T = kda_forward_chunked_host(q_cpu, k_cpu, v_cpu, g_cpu, beta_cpu, S0_cpu)  # host tensors in and out
     o = kda_decode_step(q, k, v, g, beta, S)                   # one token, S updated in place
 
+    y, conv_state = kda_short_conv(x, weight, bias, conv_state)   # the short causal convolution before it
+    y, S_T = kda_ssm_forward(x, dt, A, Bm, Cm, D, dt_bias, S0)    # the selective scan, its scalar-decay sibling
+    kda_pool_copy(pools, src, dst)                                # slots of the layers' state pools
+
 Layouts (contiguous): q, k, g [B, T, H, dk]; v, o [B, T, H, dv]; beta [B, T, H];
 states [B, H, dk, dv] fp32.  Decode drops the T axis.  dtype: bf16 or fp32 (all of q, k,
 v, g, beta share it; o gets it too).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -34,6 +39,18 @@ __all__ = [
     "kda_decode_step_paged",
     "kda_state_compose",
     "kda_output_correct",
+    "kda_short_conv",
+    "kda_short_conv_varlen",
+    "kda_short_conv_step",
+    "kda_short_conv_step_paged",
+    "kda_ssm_forward",
+    "kda_ssm_forward_varlen",
+    "kda_ssm_decode_step",
+    "kda_ssm_decode_step_paged",
+    "ssm_workspace_bytes",
+    "kda_pool_copy",
+    "kda_pool_clear",
+    "kda_pool_compact",
     "kda_get_device_status",
     "kda_status_string",
     "kda_debug_set_wait_fault",
@@ -42,6 +59,7 @@ __all__ = [
     "LIB_PATH",
     "STATUS",
     "IMPL",
+    "ACTIVATION",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -57,6 +75,7 @@ STATUS = {
 }
 DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 IMPL = {"auto": 0, "tcgen05": 1, "simt": 2}
+ACTIVATION = {None: 0, "silu": 1}
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -101,6 +120,31 @@ def lib() -> ctypes.CDLL:
         L.kda_decode_step_paged.restype = I
         L.kda_decode_step.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, P]
         L.kda_decode_step.restype = I
+        J = ctypes.c_longlong
+        L.kda_short_conv.argtypes = [P, P, P, P, P, P, I, I, I, I, J, J, I, I, P]
+        L.kda_short_conv.restype = I
+        L.kda_short_conv_varlen.argtypes = [P, P, P, P, P, P, P, I, I, I, I, J, J, I, I, P]
+        L.kda_short_conv_varlen.restype = I
+        L.kda_short_conv_step.argtypes = [P, P, P, P, P, I, I, I, J, J, I, I, P]
+        L.kda_short_conv_step.restype = I
+        L.kda_short_conv_step_paged.argtypes = [P, P, P, P, I, P, P, I, I, I, J, J, I, I, P]
+        L.kda_short_conv_step_paged.restype = I
+        L.kda_ssm_forward.argtypes = [P] * 10 + [I] * 6 + [J] * 4 + [I, I, P, ctypes.c_size_t, P]
+        L.kda_ssm_forward.restype = I
+        L.kda_ssm_forward_varlen.argtypes = [P] * 11 + [I] * 6 + [J] * 4 + [I, I, P, ctypes.c_size_t, P]
+        L.kda_ssm_forward_varlen.restype = I
+        L.kda_ssm_workspace.argtypes = [I] * 7
+        L.kda_ssm_workspace.restype = ctypes.c_size_t
+        L.kda_ssm_decode_step.argtypes = [P] * 9 + [I] * 5 + [J] * 4 + [I, P]
+        L.kda_ssm_decode_step.restype = I
+        L.kda_ssm_decode_step_paged.argtypes = [P] * 8 + [I, P, P] + [I] * 5 + [J] * 4 + [I, P]
+        L.kda_ssm_decode_step_paged.restype = I
+        L.kda_pool_copy.argtypes = [P, P, I, I, I, P, P, I, P]
+        L.kda_pool_copy.restype = I
+        L.kda_pool_clear.argtypes = [P, I, I, P, I, P]
+        L.kda_pool_clear.restype = I
+        L.kda_pool_compact.argtypes = [P, I, I, P, P, P, I, P, P]
+        L.kda_pool_compact.restype = I
         L.kda_get_device_status.argtypes = [P]
         L.kda_get_device_status.restype = I
         L.kda_status_string.argtypes = [I]
@@ -474,6 +518,379 @@ def kda_output_correct(C, S_in, o_in, *, out=None, stream=None):
                                       _stream_handle(stream))
     if rc != 0:
         raise KdaError("kda_output_correct", rc)
+    return out
+
+
+# ------------------------------------------------------------------ short convolution, scan, pools
+
+
+def _on_device(dev: torch.device):
+    """The device of the tensors made current for a call (nothing to do when it is already)."""
+    if dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {dev}")
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _empty(shape, dtype, dev, stream) -> torch.Tensor:
+    """An output or workspace in memory of the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _rows(t, name: str, lead, row, dtype, device) -> int:
+    """Check a tensor of shape lead + row whose rows are contiguous and evenly spaced (a slice of wider rows
+    is fine); returns the spacing in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape != lead + row:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {lead + row}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    stride = t.stride()
+    width = 1
+    for n, st in zip(reversed(row), reversed(stride)):
+        if n > 1 and st != width:
+            raise ValueError(f"{name} must have contiguous rows of {row}")
+        width *= n
+    if 0 in lead:
+        return width
+    ld, rows = None, 1                   # spacing found so far, and the rows it has spanned
+    for n, st in zip(reversed(lead), reversed(stride[:len(lead)])):
+        if n > 1:
+            if ld is None:
+                ld, rows = st, n
+            elif st != ld * rows:
+                raise ValueError(f"{name} must have evenly spaced rows")
+            else:
+                rows *= n
+    return width if ld is None else ld
+
+
+def _vector(t, name: str, n: int, dtype, device):
+    if t is not None:
+        _check(t, name, (n,), dtype, device)
+    return _ptr(t)
+
+
+def _dtype_code(dt) -> int:
+    if dt not in DTYPE:
+        raise ValueError(f"unsupported dtype {dt}")
+    return DTYPE[dt]
+
+
+def _conv_common(x, lead, weight, bias, y, activation, stream):
+    """The checks the convolution's forms share: (C, W, y, ldx, ldy, weight, bias pointers, activation code)."""
+    C, W = weight.shape
+    dev, dt = x.device, x.dtype
+    _dtype_code(dt)
+    if activation not in ACTIVATION:
+        raise ValueError(f"unknown activation {activation!r}")
+    _check(weight, "weight", (C, W), dt, dev)
+    b = _vector(bias, "bias", C, dt, dev)
+    ldx = _rows(x, "x", lead, (C,), dt, dev)
+    if y is None:
+        y, ldy = _empty(lead + (C,), dt, dev, stream), C
+    else:
+        ldy = _rows(y, "y", lead, (C,), dt, dev)
+    return C, W, y, ldx, ldy, weight.data_ptr(), b, ACTIVATION[activation]
+
+
+def kda_short_conv(x, weight, bias=None, state=None, *, activation="silu", y=None, state_out=None,
+                   return_state: bool = True, stream=None):
+    """The short causal convolution over x [B, T, C] (rows may be slices of wider ones): weight [C, W],
+    bias [C] or None, state [B, W-1, C] (the inputs before token 0; None for zeros).  Returns (y [B, T, C],
+    state_out [B, W-1, C] or None).  state_out may be state itself.  activation: "silu" or None."""
+    B, T = x.shape[:2]
+    C, W, y, ldx, ldy, w, b, act = _conv_common(x, (B, T), weight, bias, y, activation, stream)
+    dev, dt = x.device, x.dtype
+    if state is not None:
+        _check(state, "state", (B, W - 1, C), dt, dev)
+    if state_out is not None:
+        _check(state_out, "state_out", (B, W - 1, C), dt, dev)
+    elif return_state:
+        state_out = _empty((B, W - 1, C), dt, dev, stream)
+    with _on_device(dev):
+        rc = lib().kda_short_conv(x.data_ptr(), w, b, _ptr(state), y.data_ptr(), _ptr(state_out), B, T, C, W, ldx,
+                                  ldy, act, DTYPE[dt], _stream_handle(stream))
+    if rc != 0:
+        raise KdaError("kda_short_conv", rc)
+    return y, state_out
+
+
+def kda_short_conv_varlen(x, weight, cu_seqlens, bias=None, state=None, *, activation="silu", y=None,
+                          state_out=None, return_state: bool = True, stream=None):
+    """kda_short_conv over packed sequences: x [T_total, C], cu_seqlens int32 [N + 1] on the device (as
+    kda_forward_varlen), states [N, W-1, C].  Returns (y [T_total, C], state_out or None)."""
+    T_total = x.shape[0]
+    N = cu_seqlens.shape[0] - 1
+    C, W, y, ldx, ldy, w, b, act = _conv_common(x, (T_total,), weight, bias, y, activation, stream)
+    dev, dt = x.device, x.dtype
+    _check(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
+    if state is not None:
+        _check(state, "state", (N, W - 1, C), dt, dev)
+    if state_out is not None:
+        _check(state_out, "state_out", (N, W - 1, C), dt, dev)
+    elif return_state:
+        state_out = _empty((N, W - 1, C), dt, dev, stream)
+    with _on_device(dev):
+        rc = lib().kda_short_conv_varlen(x.data_ptr(), w, b, cu_seqlens.data_ptr(), _ptr(state), y.data_ptr(),
+                                         _ptr(state_out), N, T_total, C, W, ldx, ldy, act, DTYPE[dt],
+                                         _stream_handle(stream))
+    if rc != 0:
+        raise KdaError("kda_short_conv_varlen", rc)
+    return y, state_out
+
+
+def kda_short_conv_step(x, weight, state, bias=None, *, activation="silu", y=None, stream=None):
+    """One token for every sequence: x [B, C], state [B, W-1, C] shifted in place.  Returns y [B, C]."""
+    B = x.shape[0]
+    C, W, y, ldx, ldy, w, b, act = _conv_common(x, (B,), weight, bias, y, activation, stream)
+    dev, dt = x.device, x.dtype
+    _check(state, "state", (B, W - 1, C), dt, dev)
+    with _on_device(dev):
+        rc = lib().kda_short_conv_step(x.data_ptr(), w, b, state.data_ptr(), y.data_ptr(), B, C, W, ldx, ldy, act,
+                                       DTYPE[dt], _stream_handle(stream))
+    if rc != 0:
+        raise KdaError("kda_short_conv_step", rc)
+    return y
+
+
+def kda_short_conv_step_paged(x, weight, state_pool, slots, bias=None, *, activation="silu", y=None, stream=None):
+    """kda_short_conv_step with the states in a pool [n_slots, W-1, C]: slots int32 [B] on the device, as
+    kda_decode_step_paged."""
+    B = x.shape[0]
+    C, W, y, ldx, ldy, w, b, act = _conv_common(x, (B,), weight, bias, y, activation, stream)
+    dev, dt = x.device, x.dtype
+    n_slots = state_pool.shape[0]
+    _check(state_pool, "state_pool", (n_slots, W - 1, C), dt, dev)
+    _check(slots, "slots", (B,), torch.int32, dev)
+    with _on_device(dev):
+        rc = lib().kda_short_conv_step_paged(x.data_ptr(), w, b, state_pool.data_ptr(), n_slots, slots.data_ptr(),
+                                             y.data_ptr(), B, C, W, ldx, ldy, act, DTYPE[dt], _stream_handle(stream))
+    if rc != 0:
+        raise KdaError("kda_short_conv_step_paged", rc)
+    return y
+
+
+def _ssm_common(x, dt, A, Bm, Cm, D, dt_bias, lead, y, stream):
+    """The checks the scan's forms share: (H, G, N, P, y, row spacings, D and dt_bias pointers)."""
+    H, P = x.shape[-2:]
+    G, N = Bm.shape[-2:]
+    dev, ty = x.device, x.dtype
+    _dtype_code(ty)
+    lds = (_rows(x, "x", lead, (H, P), ty, dev), _rows(dt, "dt", lead, (H,), ty, dev),
+           _rows(Bm, "Bm", lead, (G, N), ty, dev), _rows(Cm, "Cm", lead, (G, N), ty, dev))
+    _check(A, "A", (H,), torch.float32, dev)
+    d, bias = _vector(D, "D", H, torch.float32, dev), _vector(dt_bias, "dt_bias", H, torch.float32, dev)
+    if y is None:
+        y = _empty(lead + (H, P), ty, dev, stream)
+    else:
+        _check(y, "y", lead + (H, P), ty, dev)
+    return H, G, N, P, y, lds, d, bias
+
+
+def ssm_workspace_bytes(n_seq: int, T_total: int, H: int, N: int = 128, P: int = 128, dtype=torch.bfloat16,
+                        impl: str = "auto") -> int:
+    """Bytes of device workspace kda_ssm_forward (n_seq = B, T_total = B * T) or kda_ssm_forward_varlen needs."""
+    return int(lib().kda_ssm_workspace(int(n_seq), int(T_total), int(H), int(N), int(P), _dtype_code(dtype), IMPL[impl]))
+
+
+def _ssm_workspace(workspace, n_seq, T_total, H, N, P, dt, dev, impl, stream):
+    need = lib().kda_ssm_workspace(n_seq, T_total, H, N, P, DTYPE[dt], IMPL[impl])
+    if workspace is None:
+        return _empty((need,), torch.uint8, dev, stream) if need else None
+    if not (isinstance(workspace, torch.Tensor) and workspace.device == dev and workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return workspace
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def kda_ssm_forward(x, dt, A, Bm, Cm, D=None, dt_bias=None, S0=None, *, y=None, S_T=None, return_state: bool = True,
+                    workspace=None, impl: str = "auto", stream=None):
+    """Prefill of the selective scan with one decay per head: x [B, T, H, P], dt [B, T, H], Bm, Cm
+    [B, T, G, N] (bf16 or fp32; token rows may be slices of wider ones), A, D, dt_bias [H] fp32, S0
+    [B, H, N, P] fp32.  Returns (y [B, T, H, P], S_T [B, H, N, P] or None).  S_T may be S0 itself.
+    `workspace`: a device tensor of ssm_workspace_bytes(B, B * T, ...) bytes, allocated if not given."""
+    B, T = x.shape[:2]
+    H, G, N, P, y, lds, d, bias = _ssm_common(x, dt, A, Bm, Cm, D, dt_bias, (B, T), y, stream)
+    dev, ty = x.device, x.dtype
+    if S0 is not None:
+        _check(S0, "S0", (B, H, N, P), torch.float32, dev)
+    if S_T is not None:
+        _check(S_T, "S_T", (B, H, N, P), torch.float32, dev)
+    elif return_state:
+        S_T = _empty((B, H, N, P), torch.float32, dev, stream)
+    with _on_device(dev):
+        workspace = _ssm_workspace(workspace, B, B * T, H, N, P, ty, dev, impl, stream)
+        rc = lib().kda_ssm_forward(x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), d, bias,
+                                   _ptr(S0), y.data_ptr(), _ptr(S_T), B, T, H, G, N, P, *lds, DTYPE[ty], IMPL[impl],
+                                   _ptr(workspace), _nbytes(workspace), _stream_handle(stream))
+    if rc != 0:
+        raise KdaError("kda_ssm_forward", rc)
+    return y, S_T
+
+
+def kda_ssm_forward_varlen(x, dt, A, Bm, Cm, cu_seqlens, D=None, dt_bias=None, S0=None, *, y=None, S_T=None,
+                           return_state: bool = True, workspace=None, impl: str = "auto", stream=None):
+    """kda_ssm_forward over packed sequences: x [T_total, H, P], dt [T_total, H], Bm, Cm [T_total, G, N],
+    cu_seqlens int32 [n_seq + 1] on the device, states [n_seq, H, N, P].  Returns (y [T_total, H, P], S_T or
+    None)."""
+    T_total = x.shape[0]
+    n_seq = cu_seqlens.shape[0] - 1
+    H, G, N, P, y, lds, d, bias = _ssm_common(x, dt, A, Bm, Cm, D, dt_bias, (T_total,), y, stream)
+    dev, ty = x.device, x.dtype
+    _check(cu_seqlens, "cu_seqlens", (n_seq + 1,), torch.int32, dev)
+    if S0 is not None:
+        _check(S0, "S0", (n_seq, H, N, P), torch.float32, dev)
+    if S_T is not None:
+        _check(S_T, "S_T", (n_seq, H, N, P), torch.float32, dev)
+    elif return_state:
+        S_T = _empty((n_seq, H, N, P), torch.float32, dev, stream)
+    with _on_device(dev):
+        workspace = _ssm_workspace(workspace, n_seq, T_total, H, N, P, ty, dev, impl, stream)
+        rc = lib().kda_ssm_forward_varlen(x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(),
+                                          cu_seqlens.data_ptr(), d, bias, _ptr(S0), y.data_ptr(), _ptr(S_T), n_seq,
+                                          T_total, H, G, N, P, *lds, DTYPE[ty], IMPL[impl], _ptr(workspace),
+                                          _nbytes(workspace), _stream_handle(stream))
+    if rc != 0:
+        raise KdaError("kda_ssm_forward_varlen", rc)
+    return y, S_T
+
+
+def kda_ssm_decode_step(x, dt, A, Bm, Cm, S, D=None, dt_bias=None, *, y=None, stream=None):
+    """One token of the selective scan for every (b, h): x [B, H, P], dt [B, H], Bm, Cm [B, G, N]; S
+    [B, H, N, P] fp32 updated in place.  Returns y [B, H, P]."""
+    B = x.shape[0]
+    H, G, N, P, y, lds, d, bias = _ssm_common(x, dt, A, Bm, Cm, D, dt_bias, (B,), y, stream)
+    dev, ty = x.device, x.dtype
+    _check(S, "S", (B, H, N, P), torch.float32, dev)
+    with _on_device(dev):
+        rc = lib().kda_ssm_decode_step(x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), d,
+                                       bias, S.data_ptr(), y.data_ptr(), B, H, G, N, P, *lds, DTYPE[ty],
+                                       _stream_handle(stream))
+    if rc != 0:
+        raise KdaError("kda_ssm_decode_step", rc)
+    return y
+
+
+def kda_ssm_decode_step_paged(x, dt, A, Bm, Cm, S_pool, slots, D=None, dt_bias=None, *, y=None, stream=None):
+    """kda_ssm_decode_step with the states in a pool [n_slots, H, N, P]: slots int32 [B] on the device, as
+    kda_decode_step_paged."""
+    B = x.shape[0]
+    H, G, N, P, y, lds, d, bias = _ssm_common(x, dt, A, Bm, Cm, D, dt_bias, (B,), y, stream)
+    dev, ty = x.device, x.dtype
+    n_slots = S_pool.shape[0]
+    _check(S_pool, "S_pool", (n_slots, H, N, P), torch.float32, dev)
+    _check(slots, "slots", (B,), torch.int32, dev)
+    with _on_device(dev):
+        rc = lib().kda_ssm_decode_step_paged(x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(),
+                                             d, bias, S_pool.data_ptr(), n_slots, slots.data_ptr(), y.data_ptr(), B,
+                                             H, G, N, P, *lds, DTYPE[ty], _stream_handle(stream))
+    if rc != 0:
+        raise KdaError("kda_ssm_decode_step_paged", rc)
+    return y
+
+
+def _pools(pools, name: str, device=None, beside=None):
+    """The kda_pool descriptions of a list of pool tensors [n_slots, ...]: (array, number of slots, device).
+
+    Dimension 0 counts the slots.  The others are contiguous, or dimension 1 is spaced wider (the boundary
+    states of one batch entry, S_mid[b].transpose(0, 1) of kda_forward_chunked_states).  A pool whose
+    counterpart in `beside` is spaced wider is described by the same runs."""
+    if not pools:
+        raise ValueError(f"{name} is empty")
+    flat, n_slots = [], pools[0].shape[0]
+    if device is None:
+        device = pools[0].device
+    for i, t in enumerate(pools):
+        shape, stride, es = t.shape, t.stride(), t.element_size()
+        if t.device != device:
+            raise ValueError(f"{name}: a pool is on {t.device}, expected {device}")
+        if len(shape) < 2 or shape[0] != n_slots:
+            raise ValueError(f"{name}: pools have shape [{n_slots}, ...], got {tuple(shape)}")
+        run, d = 1, len(shape) - 1
+        last = 1 if beside is not None and len(shape) > 2 and not beside[i].is_contiguous() else 0
+        while d > last and (stride[d] == run or shape[d] == 1):
+            run *= shape[d]
+            d -= 1
+        if d == 0:
+            pieces, apart = 1, 0
+        elif d == 1:
+            pieces, apart = shape[1], stride[1]
+        else:
+            raise ValueError(f"{name}: a pool's slots must be contiguous, or contiguous runs along dimension 1")
+        flat += (t.data_ptr(), (stride[0] if n_slots > 1 else max(stride[0], run)) * es, pieces, apart * es, run * es)
+    return (ctypes.c_longlong * len(flat))(*flat), n_slots, device
+
+
+def kda_pool_copy(pools, src, dst, *, src_pools=None, stream=None) -> None:
+    """Copy slots, in every pool of the list at once: slot dst[i] of each pool becomes its slot src[i] (of the
+    pool in the same place of `src_pools`, when given).  Pools are tensors [n_slots, ...]; src, dst int32 [n]
+    on the device, negative entries skip the pair.  One source may feed many destinations; a destination that
+    another pair has too, or (within one pool) reads, is left as it was and reported by the status word."""
+    if src_pools is None:
+        to, n_dst, dev = _pools(pools, "pools")
+        frm, n_src = to, n_dst
+    else:
+        if len(src_pools) != len(pools):
+            raise ValueError(f"{len(src_pools)} source pools for {len(pools)} pools")
+        for a, b in zip(pools, src_pools):
+            if a.dtype != b.dtype or a.shape[1:] != b.shape[1:]:
+                raise ValueError("a pool and its source pool must have slots of one shape and dtype")
+        to, n_dst, dev = _pools(pools, "pools", beside=src_pools)
+        frm, n_src, _ = _pools(src_pools, "src_pools", dev, beside=pools)
+    n = src.shape[0]
+    _check(src, "src", (n,), torch.int32, dev)
+    _check(dst, "dst", (n,), torch.int32, dev)
+    with _on_device(dev):
+        rc = lib().kda_pool_copy(to, frm, len(pools), n_dst, n_src, src.data_ptr(), dst.data_ptr(), n,
+                                 _stream_handle(stream))
+    if rc != 0:
+        raise KdaError("kda_pool_copy", rc)
+
+
+def kda_pool_clear(pools, slots, *, stream=None) -> None:
+    """Set the listed slots (int32 [n] on the device, negative entries skipped) of every pool to zero."""
+    to, n_slots, dev = _pools(pools, "pools")
+    n = slots.shape[0]
+    _check(slots, "slots", (n,), torch.int32, dev)
+    with _on_device(dev):
+        rc = lib().kda_pool_clear(to, len(pools), n_slots, slots.data_ptr(), n, _stream_handle(stream))
+    if rc != 0:
+        raise KdaError("kda_pool_clear", rc)
+
+
+def kda_pool_compact(pools, slots, done=None, *, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Drop the sequences that ended (done [B] bool or uint8, or slots[b] < 0) and move the others' slots to
+    the front of every pool.  Returns the new slot table, int32 [B] (-1 for ended sequences); `out` may be
+    `slots` itself.  `workspace`: int32 [n_slots + 1] on the device, allocated if not given."""
+    to, n_slots, dev = _pools(pools, "pools")
+    B = slots.shape[0]
+    _check(slots, "slots", (B,), torch.int32, dev)
+    if done is not None:
+        _check(done, "done", (B,), torch.uint8 if done.dtype == torch.uint8 else torch.bool, dev)
+    if out is None:
+        out = _empty((B,), torch.int32, dev, stream)
+    else:
+        _check(out, "out", (B,), torch.int32, dev)
+    if workspace is None:
+        workspace = _empty((n_slots + 1,), torch.int32, dev, stream)
+    else:
+        _check(workspace, "workspace", (n_slots + 1,), torch.int32, dev)
+    with _on_device(dev):
+        rc = lib().kda_pool_compact(to, len(pools), n_slots, slots.data_ptr(), _ptr(done), out.data_ptr(), B,
+                                    workspace.data_ptr(), _stream_handle(stream))
+    if rc != 0:
+        raise KdaError("kda_pool_compact", rc)
     return out
 
 

@@ -8,7 +8,7 @@
 #include <mutex>
 #include <stdint.h>
 
-#include "kda_internal.cuh"
+#include "kda_serving.cuh"
 
 // One status word per device (this module is loaded once per device context).  Kernels
 // receive its device address as an argument and set it on a timed-out wait.
@@ -350,6 +350,13 @@ int decode_impl(const void* q, const void* k, const void* v, const void* g, cons
 }
 
 }  // namespace
+
+namespace kda {
+
+int* current_status_word() { return status_word_for_current_device(); }
+unsigned long long wait_timeout_ns() { return g_timeout_ns.load(); }
+
+}  // namespace kda
 
 extern "C" {
 

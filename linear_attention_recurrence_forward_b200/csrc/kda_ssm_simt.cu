@@ -1,0 +1,139 @@
+// The selective scan in fp32 on CUDA cores, token by token (every dtype, N and P in {64, 128}): the
+// library's fp32 path, as the tensor-core kernel's operands are bf16.
+//
+//   S <- a_t S + B_t (s_t x_t)^T,  y_t = S^T C_t + D x_t,   a_t = exp(s_t A), s_t = softplus(dt_t + dt_bias)
+//
+// The P columns of S never mix, so a CTA takes one (sequence, head) and 16 columns: four warps of four
+// columns, the N rows spread over 16 lanes.  A lane holds N/16 rows x 2 columns of the state in
+// registers for the whole sequence.  There is no residual, so nothing in the token loop waits for a
+// reduction: the column sums leave through four shuffles while the next token's update runs.  Tokens
+// are staged through shared memory, 16 at a time, double-buffered: one barrier per 16 tokens.
+#include "kda_serving.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kCols = 16;        // state columns per CTA
+constexpr int kTok = 16;         // tokens per stage
+
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads)
+kda_ssm_simt_kernel(const T* __restrict__ x, const T* __restrict__ dt, const float* __restrict__ A,
+                    const T* __restrict__ Bm, const T* __restrict__ Cm, const float* __restrict__ D,
+                    const float* __restrict__ dt_bias, const float* S0, T* __restrict__ y, float* ST,
+                    const int* __restrict__ cu_seqlens, int n_seq, int T_all, int H, int rep, int P, long long ldx,
+                    long long lddt, long long ldb, long long ldc, int* status) {
+    constexpr int RPL = N / 16;          // rows per lane
+    __shared__ float bs[2][kTok][N], cs[2][kTok][N];
+    __shared__ float xs[2][kTok][kCols];
+    __shared__ float2 as[2][kTok];       // (a_t, s_t)
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nsl = P / kCols;
+    const int col0 = (int)(blockIdx.x % nsl) * kCols;
+    const size_t bh = blockIdx.x / nsl;
+    const int b = (int)(bh / H), h = (int)(bh % H), g = h / rep;
+    size_t base = (size_t)b * T_all;
+    int len = T_all;
+    if (cu_seqlens) {
+        const bool valid = packed_offsets_valid(cu_seqlens, n_seq, T_all);
+        if (!valid && tid == 0) report_status(status, KDA_ERR_INVALID_ARG);
+        base = valid ? (size_t)cu_seqlens[b] : 0;
+        len = valid ? cu_seqlens[b + 1] - cu_seqlens[b] : 0;
+    }
+    const int rl = lane & 15;                              // rows 4 rl + 64 k + (0..3)
+    const int cl = 4 * warp + 2 * (lane >> 4);             // columns cl, cl + 1 of the slice
+    float s[RPL][2];
+#pragma unroll
+    for (int i = 0; i < RPL; ++i) {
+        const int r = 4 * rl + 64 * (i / 4) + i % 4;
+        const float2 v = S0 ? *reinterpret_cast<const float2*>(S0 + (bh * N + r) * P + col0 + cl) : make_float2(0.f, 0.f);
+        s[i][0] = v.x;
+        s[i][1] = v.y;
+    }
+    const float rate = A[h], bias = dt_bias ? dt_bias[h] : 0.f, skip = D ? D[h] : 0.f;
+
+    auto stage = [&](int t0, int buf) {
+        const int n = min(kTok, len - t0);
+        for (int i = tid; i < n * N; i += kThreads) {
+            const int t = i / N, k = i % N;
+            const size_t row = base + t0 + t;
+            bs[buf][t][k] = load_elem(Bm, row * ldb + (size_t)g * N + k);
+            cs[buf][t][k] = load_elem(Cm, row * ldc + (size_t)g * N + k);
+        }
+        for (int i = tid; i < n * kCols; i += kThreads) {
+            const int t = i / kCols, k = i % kCols;
+            xs[buf][t][k] = load_elem(x, (base + t0 + t) * ldx + (size_t)h * P + col0 + k);
+        }
+        if (tid < n) {
+            const float st = softplus(load_elem(dt, (base + t0 + tid) * lddt + h) + bias);
+            as[buf][tid] = make_float2(expf(st * rate), st);
+        }
+    };
+
+    if (len > 0) stage(0, 0);
+    __syncthreads();
+    for (int t0 = 0, buf = 0; t0 < len; t0 += kTok, buf ^= 1) {
+        if (t0 + kTok < len) stage(t0 + kTok, buf ^ 1);
+        const int n = min(kTok, len - t0);
+        for (int t = 0; t < n; ++t) {
+            const float2 at = as[buf][t];
+            const float2 xv = *reinterpret_cast<const float2*>(&xs[buf][t][cl]);
+            const float u0 = at.y * xv.x, u1 = at.y * xv.y;
+            float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < RPL / 4; ++k) {
+                const float4 bv = *reinterpret_cast<const float4*>(&bs[buf][t][4 * rl + 64 * k]);
+                const float4 cv = *reinterpret_cast<const float4*>(&cs[buf][t][4 * rl + 64 * k]);
+                const float br[4] = {bv.x, bv.y, bv.z, bv.w}, cr[4] = {cv.x, cv.y, cv.z, cv.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[4 * k + i][0] = fmaf(br[i], u0, at.x * s[4 * k + i][0]);
+                    s[4 * k + i][1] = fmaf(br[i], u1, at.x * s[4 * k + i][1]);
+                    y0 = fmaf(cr[i], s[4 * k + i][0], y0);
+                    y1 = fmaf(cr[i], s[4 * k + i][1], y1);
+                }
+            }
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) {
+                y0 += __shfl_xor_sync(0xffffffffu, y0, off);
+                y1 += __shfl_xor_sync(0xffffffffu, y1, off);
+            }
+            if (rl == 0) {
+                const size_t o = ((base + t0 + t) * H + h) * P + col0 + cl;
+                store_elem(y, o, fmaf(skip, xv.x, y0));
+                store_elem(y, o + 1, fmaf(skip, xv.y, y1));
+            }
+        }
+        __syncthreads();
+    }
+    if (!ST) return;
+#pragma unroll
+    for (int i = 0; i < RPL; ++i) {
+        const int r = 4 * rl + 64 * (i / 4) + i % 4;
+        *reinterpret_cast<float2*>(ST + (bh * N + r) * P + col0 + cl) = make_float2(s[i][0], s[i][1]);
+    }
+}
+
+template <typename T>
+cudaError_t launch_t(const SsmArgs& a, cudaStream_t s) {
+    const long long grid = (long long)a.n_seq * a.H * (a.P / kCols);
+    if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    auto run = [&](auto kernel) {
+        kernel<<<(unsigned)grid, kThreads, 0, s>>>(
+            static_cast<const T*>(a.x), static_cast<const T*>(a.dt), a.A, static_cast<const T*>(a.Bm),
+            static_cast<const T*>(a.Cm), a.D, a.dt_bias, a.S0, static_cast<T*>(a.y), a.ST, a.cu_seqlens, a.n_seq, a.T,
+            a.H, a.H / a.G, a.P, a.ldx, a.lddt, a.ldb, a.ldc, a.status);
+    };
+    if (a.N == 128) run(kda_ssm_simt_kernel<T, 128>);
+    else run(kda_ssm_simt_kernel<T, 64>);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_ssm_simt(const SsmArgs& a, cudaStream_t s) {
+    return a.dtype == KDA_DTYPE_BF16 ? launch_t<__nv_bfloat16>(a, s) : launch_t<float>(a, s);
+}
+
+}  // namespace kda

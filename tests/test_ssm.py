@@ -1,0 +1,347 @@
+"""The selective scan: prompts (batched, packed), single tokens (plain, paged), against fp64."""
+import numpy as np
+import pytest
+import torch
+
+import linear_attention_recurrence_forward_b200 as kda
+from linear_attention_recurrence_forward_b200 import STATUS
+import serving_refs as ref
+from serving_refs import np64
+
+OK, INVALID, UNSUPPORTED, MISALIGNED = (STATUS[n] for n in
+                                        ("KDA_OK", "KDA_ERR_INVALID_ARG", "KDA_ERR_UNSUPPORTED",
+                                         "KDA_ERR_MISALIGNED"))
+TORCH = {"bf16": torch.bfloat16, "fp32": torch.float32}
+BASE, SZ = 0x7F0000000000, 1 << 33
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def L():
+    from linear_attention_recurrence_forward_b200 import build
+    build.build()
+    return kda.lib()
+
+
+# ---------------------------------------------------------------------- refusals (CPU)
+
+NAMES = ["x", "dt", "A", "Bm", "Cm", "D", "bias", "S0", "y", "ST", "ix", "ws"]
+AT = {n: BASE + i * SZ for i, n in enumerate(NAMES)}
+
+
+def call(L, form="batch", B=2, T=10, H=4, G=2, N=128, P=64, ldx=None, lddt=None, ldb=None, ldc=None, dtype=0, impl=0,
+         n_slots=8, ws_bytes=1 << 32, **p):
+    a = {**AT, **p}
+    ld = (ldx or H * P, lddt or H, ldb or G * N, ldc or G * N)
+    if form == "batch":
+        return L.kda_ssm_forward(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], a["D"], a["bias"], a["S0"], a["y"], a["ST"],
+                                 B, T, H, G, N, P, *ld, dtype, impl, a["ws"], ws_bytes, None)
+    if form == "varlen":
+        return L.kda_ssm_forward_varlen(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], a["ix"], a["D"], a["bias"], a["S0"],
+                                        a["y"], a["ST"], B, T, H, G, N, P, *ld, dtype, impl, a["ws"], ws_bytes, None)
+    if form == "step":
+        return L.kda_ssm_decode_step(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], a["D"], a["bias"], a["ST"], a["y"],
+                                     B, H, G, N, P, *ld, dtype, None)
+    return L.kda_ssm_decode_step_paged(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], a["D"], a["bias"], a["ST"], n_slots,
+                                       a["ix"], a["y"], B, H, G, N, P, *ld, dtype, None)
+
+
+@pytest.mark.parametrize("form", ["batch", "varlen", "step", "paged"])
+def test_refusals(L, form):
+    f = lambda **k: call(L, form, **k)  # noqa: E731
+    for k in (dict(B=0), dict(H=0), dict(G=0), dict(G=3), dict(ldx=64), dict(lddt=2), dict(ldb=64), dict(ldc=64),
+              dict(x=None), dict(dt=None), dict(A=None), dict(Bm=None), dict(Cm=None), dict(y=None)):
+        assert f(**k) == INVALID, k
+    for k in (dict(N=32), dict(P=96), dict(N=256), dict(dtype=2)):
+        assert f(**k) == UNSUPPORTED, k
+    for k in (dict(x=AT["x"] + 8), dict(dt=AT["dt"] + 1), dict(A=AT["A"] + 2), dict(Bm=AT["Bm"] + 8), dict(Cm=AT["Cm"] + 2),
+              dict(D=AT["D"] + 1), dict(bias=AT["bias"] + 2), dict(y=AT["y"] + 8), dict(ST=AT["ST"] + 4), dict(ldx=260),
+              dict(ldb=260), dict(ldc=260)):
+        assert f(**k) == MISALIGNED, k
+    for n in ("x", "dt", "A", "Bm", "Cm", "D", "bias", "ST"):
+        assert f(y=AT[n]) == INVALID, n                    # y on another argument
+    for n in ("x", "Bm"):
+        assert f(ST=AT[n] + 512) == INVALID, n
+    if form in ("batch", "varlen"):
+        assert f(T=-1) == INVALID
+        assert f(impl=9) == INVALID
+        assert f(ST=AT["S0"] + 4096) == INVALID            # partly over S0
+        assert f(y=AT["S0"]) == INVALID
+        assert f(dtype=1, impl=1) == UNSUPPORTED           # the tensor-core kernel is bf16 only
+    if form in ("varlen", "paged"):
+        assert f(ix=None) == INVALID
+        assert f(ix=AT["ix"] + 2) == MISALIGNED
+        assert f(ix=AT["y"]) == INVALID
+    if form in ("step", "paged"):
+        assert f(ST=None) == INVALID
+    if form == "paged":
+        assert f(n_slots=0) == INVALID
+
+
+def test_binding_refuses_bad_tensors():
+    x, dt, A, b = torch.zeros(2, 5, 4, 64), torch.zeros(2, 5, 4), torch.zeros(4), torch.zeros(2, 5, 2, 64)
+    with pytest.raises(ValueError):
+        kda.kda_ssm_forward(x, dt, A, b, b)                                  # not on a GPU
+    with pytest.raises(ValueError):
+        kda.kda_ssm_forward(x.half(), dt.half(), A, b.half(), b.half())
+    with pytest.raises(ValueError):
+        kda.kda_ssm_forward(x, dt, A.double(), b, b)
+    with pytest.raises(ValueError):
+        kda.kda_ssm_forward(x.transpose(2, 3), dt, A, b, b)
+    with pytest.raises(ValueError):
+        kda.kda_ssm_forward(x, dt, A, b, b.bfloat16())
+
+
+# ---------------------------------------------------------------------- GPU
+
+def case(lead, H, G, N, P, dtype, seed=0, states=None, rate=16.0, step=None):
+    """Inputs in the operators' distributions: rates -1..-rate, time steps 1e-3..1e-1 (or `step`)."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    r = lambda shape, s=1.0: torch.randn(shape, generator=g, device="cuda") * s  # noqa: E731
+    A = -(1 + (rate - 1) * torch.rand(H, generator=g, device="cuda"))
+    D = 1 + 0.1 * r((H,))
+    s = step if step is not None else torch.exp(torch.rand(H, generator=g, device="cuda") * 4.6 - 6.9)
+    bias = s + torch.log(-torch.expm1(-s)) if step is None else torch.full((H,), float(np.log(np.expm1(step))), device="cuda")
+    x, dt = r(lead + (H, P)).to(TORCH[dtype]), r(lead + (H,), 0.5).to(TORCH[dtype])
+    Bm, Cm = r(lead + (G, N)).to(TORCH[dtype]), r(lead + (G, N), N ** -0.5).to(TORCH[dtype])
+    S0 = r((states if states is not None else lead[0], H, N, P), 0.5)
+    return dict(x=x, dt=dt, A=A, Bm=Bm, Cm=Cm, D=D, dt_bias=bias, S0=S0)
+
+
+def check(y, S, c, rows, n, dtype, impl, skip=True, start=True):
+    """y [T, H, P] and S [H, N, P] of sequence n, tokens `rows` of the inputs, against fp64."""
+    f = lambda k: np64(c[k][rows])  # noqa: E731
+    T = y.shape[0]
+    ry, rS, ya, Sa = ref.scan(f("x"), f("dt"), np64(c["A"]), f("Bm"), f("Cm"), np64(c["D"]) if skip else None,
+                              np64(c["dt_bias"]) if skip else None, np64(c["S0"][n]) if start else None)
+    by, bS = ref.scan_bounds(ry, ya, Sa, T, c["Bm"].shape[-1], dtype, impl)
+    ey, eS = np.abs(np64(y) - ry), np.abs(np64(S) - rS)
+    assert np.all(ey <= by), f"y {float((ey / by).max()):.3g} of its bound"
+    assert np.all(eS <= bS), f"S {float((eS / bS).max()):.3g} of its bound"
+
+
+IMPLS = [("fp32", "simt"), ("bf16", "simt")]
+
+
+@gpu
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+@pytest.mark.parametrize("B,T,H,G,N,P", [(1, 1, 1, 1, 64, 64), (2, 7, 3, 1, 128, 64), (1, 64, 4, 2, 64, 128),
+                                         (1, 127, 2, 2, 128, 128), (3, 128, 2, 1, 128, 128), (1, 129, 6, 2, 128, 64),
+                                         (1, 300, 3, 3, 64, 64), (1, 700, 2, 1, 128, 128)])
+def test_prompt(dtype, impl, B, T, H, G, N, P):
+    c = case((B, T), H, G, N, P, dtype, seed=T)
+    y, S = kda.kda_ssm_forward(**c, impl=impl)
+    assert kda.kda_get_device_status() == 0
+    for b in range(B):
+        check(y[b], S[b], c, b, b, dtype, impl)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+@pytest.mark.parametrize("step,rate", [(2.0, 16.0), (1e-4, 1.5), (20.0, 2.0)])
+def test_strong_and_weak_decay(dtype, impl, step, rate):
+    """Time steps at which a token forgets everything before it, and at which hundreds of tokens stay."""
+    c = case((1, 260), 3, 1, 128, 64, dtype, seed=3, step=step, rate=rate)
+    y, S = kda.kda_ssm_forward(**c, impl=impl)
+    check(y[0], S[0], c, 0, 0, dtype, impl)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+def test_optional_arguments_and_state_in_place(dtype, impl):
+    c = case((2, 140), 4, 2, 128, 64, dtype, seed=5)
+    y, S = kda.kda_ssm_forward(c["x"], c["dt"], c["A"], c["Bm"], c["Cm"], impl=impl)      # no D, no bias, S0 = 0
+    for b in range(2):
+        check(y[b], S[b], c, b, b, dtype, impl, skip=False, start=False)
+    y1, S1 = kda.kda_ssm_forward(**c, impl=impl)
+    held = c["S0"].clone()
+    y2, S2 = kda.kda_ssm_forward(**{**c, "S0": held}, S_T=held, impl=impl)
+    assert S2 is held and torch.equal(y1, y2) and torch.equal(S1, S2)
+    y3, none = kda.kda_ssm_forward(**c, return_state=False, impl=impl)
+    assert none is None and torch.equal(y1, y3)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+def test_packed(dtype, impl):
+    lengths, lead, tail = [1, 0, 127, 128, 129, 5, 0, 300, 2], 3, 4
+    T, H, G, N, P = lead + sum(lengths) + tail, 4, 2, 128, 64
+    c = case((T,), H, G, N, P, dtype, seed=9, states=len(lengths))
+    for k in ("x", "dt", "Bm", "Cm"):                    # rows of no sequence reach nothing
+        c[k][:lead] = float("nan")
+        c[k][T - tail:] = float("inf")
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]) + lead, dtype=torch.int32, device="cuda")
+    y = torch.full((T, H, P), 7.0, dtype=TORCH[dtype], device="cuda")
+    y, S = kda.kda_ssm_forward_varlen(**c, cu_seqlens=cu, y=y, impl=impl)
+    assert kda.kda_get_device_status() == 0
+    at = lead
+    for n, k in enumerate(lengths):
+        check(y[at:at + k], S[n], c, slice(at, at + k), n, dtype, impl)
+        if k == 0:
+            assert torch.equal(S[n], c["S0"][n])
+        at += k
+    assert bool((y[:lead] == 7).all()) and bool((y[T - tail:] == 7).all())
+
+
+@gpu
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+@pytest.mark.parametrize("bad", [[0, 50, 130], [-2, 50, 100], [0, 70, 60]])
+def test_invalid_offsets_are_reported_not_followed(dtype, impl, bad):
+    c = case((100,), 2, 1, 128, 64, dtype, states=2)
+    y = torch.full((100, 2, 64), 7.0, dtype=TORCH[dtype], device="cuda")
+    y, S = kda.kda_ssm_forward_varlen(**c, cu_seqlens=torch.tensor(bad, dtype=torch.int32, device="cuda"), y=y, impl=impl)
+    assert kda.kda_get_device_status() == INVALID
+    assert torch.equal(S, c["S0"]) and bool((y == 7).all())
+
+
+@gpu
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+def test_slices_of_wider_rows(dtype, impl):
+    """x, B, C and dt as slices of one projection's rows equal their contiguous copies, bit for bit."""
+    B, T, H, G, N, P = 2, 200, 4, 2, 64, 64
+    c = case((B, T), H, G, N, P, dtype, seed=4)
+    wide = torch.zeros((B, T, H * P + 2 * G * N + 16), dtype=TORCH[dtype], device="cuda")
+    parts, at = {}, 0
+    for k, n in (("x", H * P), ("Bm", G * N), ("Cm", G * N), ("dt", H)):
+        wide[..., at:at + n] = c[k].flatten(2)
+        parts[k] = wide[..., at:at + n].unflatten(2, (c[k].shape[2:])) if k != "dt" else wide[..., at:at + n]
+        at += n
+    assert not parts["x"].is_contiguous()
+    y, S = kda.kda_ssm_forward(**c, impl=impl)
+    y2, S2 = kda.kda_ssm_forward(**{**c, **parts}, impl=impl)
+    assert torch.equal(y, y2) and torch.equal(S, S2)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+def test_no_tokens(dtype, impl):
+    c = case((2, 0), 2, 1, 64, 64, dtype, states=2)
+    y, S = kda.kda_ssm_forward(**c, impl=impl)
+    assert y.shape == (2, 0, 2, 64) and torch.equal(S, c["S0"])
+    _, S = kda.kda_ssm_forward(**{**c, "S0": None}, impl=impl)
+    assert bool((S == 0).all())
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,H,G,N,P", [(1, 1, 1, 64, 64), (3, 6, 2, 128, 64), (2, 5, 5, 64, 128), (5, 4, 1, 128, 128)])
+def test_steps(dtype, B, H, G, N, P):
+    T = 4
+    c = case((B, T), H, G, N, P, dtype, seed=B)
+    S = c["S0"].clone()
+    n_slots = B + 2
+    slots = torch.randperm(n_slots, device="cuda")[:B].to(torch.int32)
+    pool = torch.full((n_slots, H, N, P), 3.0, device="cuda")
+    pool[slots.long()] = S
+    ys = []
+    for t in range(T):
+        one = {k: c[k][:, t] for k in ("x", "dt", "Bm", "Cm")}
+        y = kda.kda_ssm_decode_step(**one, A=c["A"], S=S, D=c["D"], dt_bias=c["dt_bias"])
+        yp = kda.kda_ssm_decode_step_paged(**{k: v.contiguous() for k, v in one.items()}, A=c["A"], S_pool=pool, slots=slots,
+                                           D=c["D"], dt_bias=c["dt_bias"])
+        assert torch.equal(y, yp)
+        ys.append(y)
+    y = torch.stack(ys, 1)
+    for b in range(B):
+        check(y[b], S[b], c, b, b, dtype, "simt")
+    assert torch.equal(pool[slots.long()], S) and kda.kda_get_device_status() == 0
+    free = torch.ones(n_slots, dtype=torch.bool, device="cuda")
+    free[slots.long()] = False
+    assert bool((pool[free] == 3).all())
+
+
+@gpu
+def test_paged_step_skips_and_reports():
+    c = case((3,), 2, 1, 64, 64, "bf16", states=4)
+    pool, before = c.pop("S0"), None
+    before = pool.clone()
+    slots = torch.tensor([2, -1, 4], dtype=torch.int32, device="cuda")
+    y = torch.full((3, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    kda.kda_ssm_decode_step_paged(**c, S_pool=pool, slots=slots, y=y)
+    assert kda.kda_get_device_status() == INVALID
+    assert bool((y[1:] == 7).all()) and not bool((y[0] == 7).all())
+    assert torch.equal(pool[[0, 1, 3]], before[[0, 1, 3]])
+
+
+@gpu
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+def test_on_a_stream_and_in_a_graph(dtype, impl):
+    c = case((1, 300), 2, 1, 128, 64, dtype, seed=8)
+    y0, S0 = kda.kda_ssm_forward(**c, impl=impl)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y1, S1 = kda.kda_ssm_forward(**c, impl=impl, stream=side)
+    side.synchronize()
+    assert torch.equal(y0, y1) and torch.equal(S0, S1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        yg, Sg = kda.kda_ssm_forward(**c, impl=impl)
+    for _ in range(2):
+        yg.zero_()
+        graph.replay()
+        assert torch.equal(y0, yg) and torch.equal(S0, Sg)
+
+
+@gpu
+def test_a_layer_as_it_is_served():
+    """Convolution, scan, a fork of both states to three continuations, single tokens, compaction: each
+    sequence's outputs equal one prompt over all its tokens."""
+    T, more, H, G, N, P = 150, 6, 4, 2, 64, 64
+    C, n_slots = H * P + 2 * G * N, 12
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    w, b = (r(C, 4) * 0.5).bfloat16(), (r(C) * 0.1).bfloat16()
+    A, D, bias = -1 - 3 * torch.rand(H, generator=g, device="cuda"), r(H), r(H) - 3
+    prompt, tails = r(1, T, C).bfloat16(), r(3, more, C).bfloat16()
+    dt_p, dt_t = r(1, T, H).bfloat16(), r(3, more, H).bfloat16()
+    cut = lambda u: (u[..., :H * P].unflatten(-1, (H, P)), u[..., H * P:H * P + G * N].unflatten(-1, (G, N)),  # noqa: E731
+                     u[..., H * P + G * N:].unflatten(-1, (G, N)))
+    conv_pool = torch.zeros((n_slots, 3, C), dtype=torch.bfloat16, device="cuda")
+    scan_pool = torch.zeros((n_slots, H, N, P), device="cuda")
+    u, conv_pool[7:8] = kda.kda_short_conv(prompt, w, b)
+    x, Bm, Cm = cut(u)
+    _, scan_pool[7:8] = kda.kda_ssm_forward(x, dt_p, A, Bm, Cm, D, bias)
+    ids = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    kda.kda_pool_copy([conv_pool, scan_pool], ids(7, 7), ids(10, 3))
+    slots = ids(7, 10, 3)
+    got = []
+    for t in range(more):
+        if t == more // 2:
+            slots = kda.kda_pool_compact([conv_pool, scan_pool], slots)
+            assert sorted(slots.tolist()) == [0, 1, 2]
+        u = kda.kda_short_conv_step_paged(tails[:, t], w, conv_pool, slots, b)
+        x, Bm, Cm = cut(u)
+        got.append(kda.kda_ssm_decode_step_paged(x, dt_t[:, t], A, Bm, Cm, scan_pool, slots, D, bias))
+    got = torch.stack(got, 1)
+    assert kda.kda_get_device_status() == 0
+    for i in range(3):
+        whole = torch.cat([prompt, tails[i:i + 1]], 1)
+        u, _ = kda.kda_short_conv(whole, w, b)
+        x, Bm, Cm = cut(u)
+        ry, rS, ya, Sa = ref.scan(np64(x[0]), np64(torch.cat([dt_p, dt_t[i:i + 1]], 1)[0]), np64(A), np64(Bm[0]), np64(Cm[0]),
+                                  np64(D), np64(bias))
+        by, bS = ref.scan_bounds(ry, ya, Sa, T + more, N, "bf16", "tcgen05")
+        assert np.all(np.abs(np64(got[i]) - ry[T:]) <= by[T:]), i
+        assert np.all(np.abs(np64(scan_pool[int(slots[i])]) - rS) <= bS), i
+
+
+@gpu
+def test_convolution_feeds_the_kda_prefill():
+    """q, k, v through the convolution, then the prefill with the fused prologue: parity with the oracle on
+    the convolution's outputs, and the state carried over two parts of the prompt."""
+    import oracle
+    from helpers import max_rel_err
+    B, T, H, d = 1, 130, 2, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    proj, w = r(B, T, 3 * H * d), (r(3 * H * d, 4) * 0.5)
+    zg, zb = r(B, T, H, d), r(B, T, H)
+    u, _ = kda.kda_short_conv(proj, w)
+    q, k, v = (t.unflatten(-1, (H, d)).contiguous() for t in u.split(H * d, -1))
+    o, S = kda.kda_forward_chunked_fused(q, k, v, zg, zb)
+    o_ref, S_ref = oracle.forward_fused(q, k, v, zg, zb)
+    assert max_rel_err(np64(o), o_ref) <= 2e-2 and max_rel_err(np64(S), S_ref) <= 2e-2
