@@ -455,12 +455,13 @@ KDA_API int kda_short_conv_step_paged(const void* x, const void* weight, const v
  *   y       : [B, T, H, P]  dtype output, contiguous
  *   S_T     : [B, H, N, P]  fp32 output, or NULL; may be S0 itself; no other overlap
  *   N, P    : 64 or 128.  G divides H.
- *   impl    : kda_impl.  KDA_IMPL_AUTO and KDA_IMPL_SIMT run the token-serial fp32 kernel;
- *             KDA_IMPL_TCGEN05 is refused.
+ *   impl    : kda_impl.  KDA_IMPL_AUTO runs the chunked tensor-core kernel for bf16 and the
+ *             token-serial fp32 kernel for fp32; KDA_IMPL_TCGEN05 refuses fp32.
  *   workspace, workspace_bytes : DEVICE memory of at least kda_ssm_workspace(...) bytes, 16-byte
  *             aligned (NULL when that is 0), not used by anything else until the work is done.
  *
- * T == 0 copies S0 to S_T.
+ * The tensor-core kernel forms whole 128-token blocks: a non-finite value in one token's x or B may
+ * reach the outputs of other tokens of its block, earlier ones too.  T == 0 copies S0 to S_T.
  */
 KDA_API int kda_ssm_forward(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
                             const float* D, const float* dt_bias, const float* S0, void* y, float* S_T, int B,

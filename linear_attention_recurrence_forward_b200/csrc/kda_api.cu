@@ -355,6 +355,7 @@ namespace kda {
 
 int* current_status_word() { return status_word_for_current_device(); }
 unsigned long long wait_timeout_ns() { return g_timeout_ns.load(); }
+int wait_fault_mode() { return g_skip_handoff.load(); }
 
 }  // namespace kda
 

@@ -42,11 +42,14 @@ struct SsmArgs {
     int* status;
     unsigned long long timeout_ns;
     void* workspace;
+    int skip_handoff;          // test hook: 1 = the tensor-core kernel's first hand-off is left out
 };
 
 cudaError_t launch_short_conv(const ConvArgs& a, cudaStream_t s);
 cudaError_t launch_short_conv_step(const ConvArgs& a, cudaStream_t s);
 cudaError_t launch_ssm_simt(const SsmArgs& a, cudaStream_t s);
+bool ssm_tc_supports(const SsmArgs& a);
+cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t s);
 cudaError_t launch_ssm_decode(const SsmArgs& a, cudaStream_t s);
 cudaError_t launch_pool_copy(const kda_pool* dst, const kda_pool* src, int n_pools, int n_dst, int n_src,
                              const int* src_idx, const int* dst_idx, int n, int* status, cudaStream_t s);
@@ -59,6 +62,7 @@ cudaError_t launch_pool_compact(const kda_pool* pools, int n_pools, int n_slots,
 // The status word of the current device (null on failure) and the limit of device-side waits.
 int* current_status_word();
 unsigned long long wait_timeout_ns();
+int wait_fault_mode();     // kda_debug_set_wait_fault
 
 // softplus(v) = log(1 + e^v) without overflow or cancellation
 __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }

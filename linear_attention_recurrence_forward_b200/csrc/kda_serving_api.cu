@@ -114,7 +114,8 @@ int run_ssm(kda::SsmArgs& a, size_t tokens, int impl, size_t workspace_bytes, cu
     if (impl != KDA_IMPL_AUTO && impl != KDA_IMPL_TCGEN05 && impl != KDA_IMPL_SIMT) return KDA_ERR_INVALID_ARG;
     const int rc = check_ssm(a, tokens, a.n_seq, false);
     if (rc != KDA_OK) return rc;
-    if (impl == KDA_IMPL_TCGEN05) return KDA_ERR_UNSUPPORTED;
+    const bool tc = impl != KDA_IMPL_SIMT && kda::ssm_tc_supports(a);
+    if (impl == KDA_IMPL_TCGEN05 && !tc) return KDA_ERR_UNSUPPORTED;
     (void)workspace_bytes;
     if (tokens == 0 && !a.cu_seqlens) {
         if (!a.ST || a.S0 == a.ST) return KDA_OK;
@@ -125,7 +126,8 @@ int run_ssm(kda::SsmArgs& a, size_t tokens, int impl, size_t workspace_bytes, cu
     }
     a.status = kda::current_status_word();
     if (!a.status) return KDA_ERR_CUDA;
-    return kda::launch_ssm_simt(a, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    const cudaError_t e = tc ? kda::launch_ssm_tc(a, stream) : kda::launch_ssm_simt(a, stream);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------ state pools
@@ -252,7 +254,7 @@ int kda_ssm_forward(const void* x, const void* dt, const float* A, const void* B
                     void* workspace, size_t workspace_bytes, struct CUstream_st* stream) {
     if (B <= 0 || T < 0 || (double)B * T > 2.0e9) return KDA_ERR_INVALID_ARG;
     kda::SsmArgs a{x, dt, A, Bm, Cm, D, dt_bias, S0, y, S_T, nullptr, B, T, H, G, N, P, ldx, lddt, ldb, ldc, dtype,
-                   nullptr, 0, nullptr, kda::wait_timeout_ns(), workspace};
+                   nullptr, 0, nullptr, kda::wait_timeout_ns(), workspace, kda::wait_fault_mode()};
     return run_ssm(a, (size_t)B * T, impl, workspace_bytes, stream);
 }
 
@@ -261,9 +263,9 @@ int kda_ssm_forward_varlen(const void* x, const void* dt, const float* A, const 
                            float* S_T, int n_seq, int T_total, int H, int G, int N, int P, long long ldx,
                            long long lddt, long long ldb, long long ldc, int dtype, int impl, void* workspace,
                            size_t workspace_bytes, struct CUstream_st* stream) {
-    if (n_seq <= 0 || T_total < 0 || !cu_seqlens) return KDA_ERR_INVALID_ARG;
+    if (n_seq <= 0 || T_total < 0 || T_total > 2000000000 || !cu_seqlens) return KDA_ERR_INVALID_ARG;
     kda::SsmArgs a{x, dt, A, Bm, Cm, D, dt_bias, S0, y, S_T, cu_seqlens, n_seq, T_total, H, G, N, P, ldx, lddt, ldb,
-                   ldc, dtype, nullptr, 0, nullptr, kda::wait_timeout_ns(), workspace};
+                   ldc, dtype, nullptr, 0, nullptr, kda::wait_timeout_ns(), workspace, kda::wait_fault_mode()};
     return run_ssm(a, (size_t)T_total, impl, workspace_bytes, stream);
 }
 
@@ -276,7 +278,7 @@ int kda_ssm_decode_step(const void* x, const void* dt, const float* A, const voi
                         const float* dt_bias, float* S, void* y, int B, int H, int G, int N, int P, long long ldx,
                         long long lddt, long long ldb, long long ldc, int dtype, struct CUstream_st* stream) {
     kda::SsmArgs a{x, dt, A, Bm, Cm, D, dt_bias, S, y, S, nullptr, B, 1, H, G, N, P, ldx, lddt, ldb, ldc, dtype,
-                   nullptr, 0, nullptr, kda::wait_timeout_ns(), nullptr};
+                   nullptr, 0, nullptr, kda::wait_timeout_ns(), nullptr, 0};
     const int rc = B <= 0 ? KDA_ERR_INVALID_ARG : check_ssm(a, B, B, true);
     if (rc != KDA_OK) return rc;
     a.status = kda::current_status_word();
@@ -290,7 +292,7 @@ int kda_ssm_decode_step_paged(const void* x, const void* dt, const float* A, con
                               long long ldb, long long ldc, int dtype, struct CUstream_st* stream) {
     if (!slots || n_slots <= 0 || B <= 0) return KDA_ERR_INVALID_ARG;
     kda::SsmArgs a{x, dt, A, Bm, Cm, D, dt_bias, S_pool, y, S_pool, nullptr, B, 1, H, G, N, P, ldx, lddt, ldb, ldc,
-                   dtype, slots, n_slots, nullptr, kda::wait_timeout_ns(), nullptr};
+                   dtype, slots, n_slots, nullptr, kda::wait_timeout_ns(), nullptr, 0};
     const int rc = check_ssm(a, B, n_slots, true);
     if (rc != KDA_OK) return rc;
     a.status = kda::current_status_word();

@@ -122,7 +122,7 @@ def check(y, S, c, rows, n, dtype, impl, skip=True, start=True):
     assert np.all(eS <= bS), f"S {float((eS / bS).max()):.3g} of its bound"
 
 
-IMPLS = [("fp32", "simt"), ("bf16", "simt")]
+IMPLS = [("fp32", "simt"), ("bf16", "simt"), ("bf16", "tcgen05")]
 
 
 @gpu
