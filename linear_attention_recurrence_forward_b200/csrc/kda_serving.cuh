@@ -49,6 +49,7 @@ cudaError_t launch_short_conv(const ConvArgs& a, cudaStream_t s);
 cudaError_t launch_short_conv_step(const ConvArgs& a, cudaStream_t s);
 cudaError_t launch_ssm_simt(const SsmArgs& a, cudaStream_t s);
 bool ssm_tc_supports(const SsmArgs& a);
+size_t ssm_tc_workspace(int n_seq, long long T_total, int H, int N, int P);
 cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t s);
 cudaError_t launch_ssm_decode(const SsmArgs& a, cudaStream_t s);
 cudaError_t launch_pool_copy(const kda_pool* dst, const kda_pool* src, int n_pools, int n_dst, int n_src,

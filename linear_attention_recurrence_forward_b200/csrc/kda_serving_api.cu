@@ -116,7 +116,22 @@ int run_ssm(kda::SsmArgs& a, size_t tokens, int impl, size_t workspace_bytes, cu
     if (rc != KDA_OK) return rc;
     const bool tc = impl != KDA_IMPL_SIMT && kda::ssm_tc_supports(a);
     if (impl == KDA_IMPL_TCGEN05 && !tc) return KDA_ERR_UNSUPPORTED;
-    (void)workspace_bytes;
+    const size_t need = tc ? kda::ssm_tc_workspace(a.n_seq, (long long)tokens, a.H, a.N, a.P) : 0;
+    if (need > 0) {
+        if (!a.workspace || workspace_bytes < need) return KDA_ERR_INVALID_ARG;
+        if (!aligned16(a.workspace)) return KDA_ERR_MISALIGNED;
+        const size_t es = elem_size(a.dtype), HP = (size_t)a.H * a.P, GN = (size_t)a.G * a.N;
+        const size_t sbytes = (size_t)a.n_seq * HP * a.N * sizeof(float);
+        const Range rw = range_of(a.workspace, need);
+        const Range others[] = {rows_of(a.x, tokens, HP, a.ldx, es), rows_of(a.dt, tokens, a.H, a.lddt, es),
+                                rows_of(a.Bm, tokens, GN, a.ldb, es), rows_of(a.Cm, tokens, GN, a.ldc, es),
+                                range_of(a.y, tokens * HP * es), range_of(a.S0, sbytes), range_of(a.ST, sbytes),
+                                range_of(a.A, a.H * sizeof(float)), range_of(a.D, a.H * sizeof(float)),
+                                range_of(a.dt_bias, a.H * sizeof(float)),
+                                range_of(a.cu_seqlens, ((size_t)a.n_seq + 1) * sizeof(int))};
+        for (const Range& r : others)
+            if (overlaps(rw, r)) return KDA_ERR_INVALID_ARG;
+    }
     if (tokens == 0 && !a.cu_seqlens) {
         if (!a.ST || a.S0 == a.ST) return KDA_OK;
         const size_t sbytes = (size_t)a.n_seq * a.H * a.N * a.P * sizeof(float);
@@ -270,8 +285,10 @@ int kda_ssm_forward_varlen(const void* x, const void* dt, const float* A, const 
 }
 
 size_t kda_ssm_workspace(int n_seq, int T_total, int H, int N, int P, int dtype, int impl) {
-    (void)n_seq; (void)T_total; (void)H; (void)N; (void)P; (void)dtype; (void)impl;
-    return 0;
+    if (n_seq <= 0 || T_total < 0 || H <= 0 || !head_dim_ok(N) || !head_dim_ok(P) || dtype != KDA_DTYPE_BF16 ||
+        (impl != KDA_IMPL_AUTO && impl != KDA_IMPL_TCGEN05))
+        return 0;
+    return kda::ssm_tc_workspace(n_seq, T_total, H, N, P);
 }
 
 int kda_ssm_decode_step(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm, const float* D,

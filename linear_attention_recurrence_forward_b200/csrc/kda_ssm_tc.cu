@@ -17,16 +17,20 @@
 // diagonal blocks take an exponential per element.
 //
 // Precision.  Outputs are bf16: S is read as a bf16 operand and Q is rounded to bf16, one rounding of
-// each term of y.  The state itself is fp32 and stays accurate to 2^-16 of each term: B and x are exact
-// bf16 operands and the weighted x enters as the sum of two bf16 values, hi and lo.
+// each term of y.  The state itself is fp32: B and x are exact bf16 operands, and a weight w = w1 + w2
+// (two bf16 values, off by at most 2^-16 w) makes the weighted x the sum of two bf16 values,
+// hi = x w1 rounded and lo = x w2 + (x w1 - hi) rounded (x w1 - hi is exact), so a term of the state is
+// off by at most 3 * 2^-16 of itself.  One bf16 value would leave 2^-8, a third product costs a fifth
+// more tensor time.
 //
 // What bounds it: HBM moves 64 KB of x and y per chunk of a 128-column tile (2.8K cycles at the
 // measured copy rate), the tensor core needs 2.5K cycles, and its operands with the tiles' own traffic
-// about 3.7K cycles of shared memory, so operands are kept out of shared memory where a product allows:
+// about 3.5K cycles of shared memory, so operands are kept out of shared memory where a product allows:
 // Q and the weighted x are tensor-memory operands, and the state is held transposed (lanes = value
-// columns) for that.
+// columns) for that.  The weighted x is transposed on its way by ldmatrix and the 16x128b stores, whose
+// fragments have one layout.
 //
-// Warps (18): 0-3 state and outputs, 4-7 decays and weighted x, 8-15 Q, 16 products, 17 loads.
+// Warps (18): 0-3 state, 4-7 decays and weighted x, 8-15 Q and outputs, 16 products, 17 loads.
 // Tensor memory (512 columns): S^T, Y, G (then Q in its place), weighted x hi and lo.
 // Order of the products: Y = C S | S += hi | Y += Q X | S += lo | next G.  The scaling of Y runs under
 // the hi part, Y's store under the lo part, the state's conversion under the next G.
@@ -68,11 +72,11 @@ constexpr uint32_t SMEM_DYN = OFF_S + kTile + 1024;
 // tensor memory columns
 constexpr uint32_t TM_S = 0, TM_Y = 128, TM_G = 256, TM_HI = 384, TM_LO = 448, TM_COLS = 512;
 
-struct Scalars {                             // of one chunk, per head of the tile
-    float L[2][kTok];                        // running sum within the token's 32-token block, inclusive
+struct __align__(16) Scalars {               // of one chunk, per head of the tile
+    float neg[2][kTok];                      // -(running sum within the token's 32-token block, inclusive)
     float col[2][kTok];                      // s_j 2^{block end - L_j}
     float step[2][kTok];                     // s_j
-    float w[2][kTok];                        // s_j 2^{chunk end - L_j}
+    uint16_t w1[2][kTok], w2[2][kTok];       // s_j 2^{chunk end - L_j} as a sum of two bf16 values
     float total[2][4];                       // sums of the four blocks
 };
 
@@ -118,7 +122,8 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// A: 128 tokens of K in 64 packed columns; B: MN-major tile whose K axis is the tokens
+// A: 128 tokens of K in 64 packed columns; B: MN-major tile whose K axis is the tokens.  The K steps are unrolled (a
+// rolled loop issues a product every 160 cycles, the tensor core takes one every 64).
 __device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, uint32_t b_base, uint32_t idesc, bool accumulate) {
     const uint64_t bd = smem_desc_sw128(b_base, ATOM, 1024u);
 #pragma unroll
@@ -130,30 +135,92 @@ template <int N>
 __device__ __forceinline__ void issue_ss(uint32_t d, uint32_t a_base, uint32_t b_base, uint32_t idesc) {
     issue_mma<N / 16, false, ATOM, false, ATOM>(d, a_base, b_base, idesc, false);
 }
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// two products a b as bf16x2
+__device__ __forceinline__ uint32_t mul2_bf16x2(uint64_t a, uint64_t b) {
+    const uint64_t r = mul2(a, b);
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r));
+    return bf16x2(lo, hi);
+}
+// v[0..n) *= e
+template <int NV>
+__device__ __forceinline__ void scale_by(float* v, float e) {
+    const uint64_t e2 = pair2(e, e);
+#pragma unroll
+    for (int i = 0; i < NV; i += 2) {
+        const uint64_t r = mul2(pair2(v[i], v[i + 1]), e2);
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(v[i]), "=f"(v[i + 1]) : "l"(r));
+    }
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+// four 8 x 8 bf16 matrices, transposed: thread i gets rows 2(i%4), 2(i%4)+1 of column i/4 of each
+__device__ __forceinline__ void ldmatrix4t(uint32_t addr, uint32_t (&m)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(m[0]), "=r"(m[1]), "=r"(m[2]), "=r"(m[3]) : "r"(addr) : "memory");
+}
+// 16 lanes x 16 columns: register 2k of thread i goes to lane i/4, column 4k + i%4, register 2k+1 to lane 8 + i/4
+__device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t* u) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* u) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
                  "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
                  : "memory");
 }
 
-// TMEM -> registers, 32 columns, complete on return.  Load and wait are one statement: between two, the
+// TMEM -> registers, 64 columns, complete on return.  Load and wait are one statement: between two, the
 // compiler may move or spill registers that the load has not written yet.
-__device__ __forceinline__ void tmem_read32(uint32_t taddr, float* r) {
+__device__ __forceinline__ void tmem_read64(uint32_t taddr, float* r) {
     uint32_t* u = reinterpret_cast<uint32_t*>(r);
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
-          "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]),
-          "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]),
-          "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "=&r"(u[0]), "=&r"(u[1]), "=&r"(u[2]), "=&r"(u[3]), "=&r"(u[4]), "=&r"(u[5]), "=&r"(u[6]), "=&r"(u[7]),
+          "=&r"(u[8]), "=&r"(u[9]), "=&r"(u[10]), "=&r"(u[11]), "=&r"(u[12]), "=&r"(u[13]), "=&r"(u[14]), "=&r"(u[15]),
+          "=&r"(u[16]), "=&r"(u[17]), "=&r"(u[18]), "=&r"(u[19]), "=&r"(u[20]), "=&r"(u[21]), "=&r"(u[22]), "=&r"(u[23]),
+          "=&r"(u[24]), "=&r"(u[25]), "=&r"(u[26]), "=&r"(u[27]), "=&r"(u[28]), "=&r"(u[29]), "=&r"(u[30]), "=&r"(u[31]),
+          "=&r"(u[32]), "=&r"(u[33]), "=&r"(u[34]), "=&r"(u[35]), "=&r"(u[36]), "=&r"(u[37]), "=&r"(u[38]), "=&r"(u[39]),
+          "=&r"(u[40]), "=&r"(u[41]), "=&r"(u[42]), "=&r"(u[43]), "=&r"(u[44]), "=&r"(u[45]), "=&r"(u[46]), "=&r"(u[47]),
+          "=&r"(u[48]), "=&r"(u[49]), "=&r"(u[50]), "=&r"(u[51]), "=&r"(u[52]), "=&r"(u[53]), "=&r"(u[54]), "=&r"(u[55]),
+          "=&r"(u[56]), "=&r"(u[57]), "=&r"(u[58]), "=&r"(u[59]), "=&r"(u[60]), "=&r"(u[61]), "=&r"(u[62]), "=&r"(u[63])
         : "r"(taddr)
         : "memory");
 }
-// Four runs of 16 columns, 32 apart.
-__device__ __forceinline__ void tmem_read4x16(uint32_t taddr, float* r) {
+__device__ __forceinline__ void tmem_write32(uint32_t taddr, const float* r) {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
+          "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]),
+          "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]),
+          "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
+        : "memory");
+}
+// Three runs of 16 columns, 32 apart, and a fourth at `other`.
+__device__ __forceinline__ void tmem_read3x16(uint32_t taddr, float* r, uint32_t other, float* r2) {
     uint32_t* u = reinterpret_cast<uint32_t*>(r);
+    uint32_t* w = reinterpret_cast<uint32_t*>(r2);
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%64];\n\t"
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%65];\n\t"
@@ -166,9 +233,9 @@ __device__ __forceinline__ void tmem_read4x16(uint32_t taddr, float* r) {
           "=&r"(u[24]), "=&r"(u[25]), "=&r"(u[26]), "=&r"(u[27]), "=&r"(u[28]), "=&r"(u[29]), "=&r"(u[30]), "=&r"(u[31]),
           "=&r"(u[32]), "=&r"(u[33]), "=&r"(u[34]), "=&r"(u[35]), "=&r"(u[36]), "=&r"(u[37]), "=&r"(u[38]), "=&r"(u[39]),
           "=&r"(u[40]), "=&r"(u[41]), "=&r"(u[42]), "=&r"(u[43]), "=&r"(u[44]), "=&r"(u[45]), "=&r"(u[46]), "=&r"(u[47]),
-          "=&r"(u[48]), "=&r"(u[49]), "=&r"(u[50]), "=&r"(u[51]), "=&r"(u[52]), "=&r"(u[53]), "=&r"(u[54]), "=&r"(u[55]),
-          "=&r"(u[56]), "=&r"(u[57]), "=&r"(u[58]), "=&r"(u[59]), "=&r"(u[60]), "=&r"(u[61]), "=&r"(u[62]), "=&r"(u[63])
-        : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
+          "=&r"(w[0]), "=&r"(w[1]), "=&r"(w[2]), "=&r"(w[3]), "=&r"(w[4]), "=&r"(w[5]), "=&r"(w[6]), "=&r"(w[7]),
+          "=&r"(w[8]), "=&r"(w[9]), "=&r"(w[10]), "=&r"(w[11]), "=&r"(w[12]), "=&r"(w[13]), "=&r"(w[14]), "=&r"(w[15])
+        : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(other)
         : "memory");
 }
 
@@ -211,15 +278,15 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 template <int N, int P, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThreads, 1)
 kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
-                  const __grid_constant__ CUtensorMap tm_c, const Params p) {
+                  const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_y, const Params p) {
     constexpr int NH = P == 64 ? 2 : 1;      // heads per tile
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_u32(smem_raw);
     uint8_t* sm = smem_raw + (((raw_base + 1023u) & ~1023u) - raw_base);
     const uint32_t sb = smem_u32(sm);
     __shared__ Scalars scal[2];
-    __shared__ uint64_t full[kStages], empty[kStages], full_c, bar_scal[2], bar_g, bar_cs, bar_upd, bar_px, bar_state, bar_scaled,
-        bar_w, bar_q, bar_drain;
+    __shared__ uint64_t full[kStages], empty[kStages], full_c, bar_scal[2], bar_g, bar_cs, bar_upd, bar_px, bar_state, bar_w, bar_q,
+        bar_yfree, bar_staged, bar_drain;
     __shared__ uint32_t tmem_base_s;
     __shared__ volatile int abort_s;
     __shared__ int seq_s, seg_s;
@@ -300,13 +367,15 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         mbar_init(&bar_upd, 1);
         mbar_init(&bar_px, 1);
         mbar_init(&bar_state, kStateWarps);
-        mbar_init(&bar_scaled, kStateWarps);
+        mbar_init(&bar_yfree, kScoreWarps);
+        mbar_init(&bar_staged, kScoreWarps);
         mbar_init(&bar_w, kDecayWarps);
         mbar_init(&bar_q, kScoreWarps);
         mbar_init(&bar_drain, 1);
         fence_mbar_init();
         abort_s = 0;
         prefetch_tensormap(&tm_x); prefetch_tensormap(&tm_b); prefetch_tensormap(&tm_c);
+        prefetch_tensormap(&tm_y);
     }
     if (warp == 0) {
         tmem_alloc(&tmem_base_s, TM_COLS);
@@ -321,26 +390,53 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     const int quarter = warp & 3;
 
     if (warp == kLoadWarp) {
-        // ------------------------------------------------------------ loads
+        // ------------------------------------------------------------ loads, and the stores of y
         if (lane == 0) {
+            constexpr int na = N / 64;
             int issued = 0, issued_c = 0;
-            for (int c = 0; c < chunks; ++c) {
-                const int st = c % kStages;
-                if (c >= kStages && !wait.one(&empty[st], (uint32_t)(c / kStages - 1) & 1)) break;
+            auto load_bx = [&](int c) {
+                const int st = c % kStages, t = row0 + c * kTok;
                 uint8_t* s = sm + st * kStageBytes;
-                const int t = row0 + c * kTok, na = N / 64;
                 mbar_arrive_expect_tx(&full[st], ATOM * (2 + na));
                 for (int i = 0; i < na; ++i) tma_load_4d(s + OFF_B + i * ATOM, &tm_b, &full[st], 64 * i, g, t, row_seq);
                 for (int i = 0; i < 2; ++i)
                     tma_load_4d(s + OFF_X + i * ATOM, &tm_x, &full[st], NH == 2 ? 0 : 64 * i, NH == 2 && i ? h1 : h0, t, row_seq);
                 ++issued;
-                if (STATE_ONLY) continue;
-                if (c > 0 && !wait.one(&bar_cs, (uint32_t)(c - 1) & 1)) break;
+            };
+            auto load_c = [&](int c) {
                 mbar_arrive_expect_tx(&full_c, ATOM * na);
-                for (int i = 0; i < na; ++i) tma_load_4d(sm + OFF_C + i * ATOM, &tm_c, &full_c, 64 * i, g, t, row_seq);
+                for (int i = 0; i < na; ++i)
+                    tma_load_4d(sm + OFF_C + i * ATOM, &tm_c, &full_c, 64 * i, g, row0 + c * kTok, row_seq);
                 ++issued_c;
+            };
+            if (chunks > 0) load_bx(0);
+            if (chunks > 0 && !STATE_ONLY) load_c(0);
+            if (chunks > 1) load_bx(1);
+            for (int c = 0; c < chunks; ++c) {
+                const int st = c % kStages;
+                if (!STATE_ONLY) {
+                    if (c + 1 < chunks) {
+                        if (!wait.one(&bar_cs, c & 1)) break;            // the chunk's C is used up
+                        load_c(c + 1);
+                    }
+                    // y of the chunk, staged in its x tile: whole tiles, clipped at the end of the tensor
+                    if (!wait.one(&bar_staged, c & 1)) break;
+                    if (!p.cu_seqlens || len - c * kTok >= kTok) {
+                        for (int i = 0; i < 2; ++i)
+                            if (!(NH == 2 && i == 1 && h1 == h0))
+                                tma_store_4d(&tm_y, sm + st * kStageBytes + OFF_X + i * ATOM, NH == 2 ? 0 : 64 * i,
+                                             NH == 2 && i ? h1 : h0, row0 + c * kTok, row_seq);
+                        bulk_commit_group();
+                        bulk_wait_read_all();
+                    }
+                }
+                if (c + kStages < chunks) {
+                    if (!wait.one(&empty[st], (uint32_t)(c / kStages) & 1)) break;
+                    load_bx(c + kStages);
+                }
             }
-            // nothing may be in flight when the CTA exits (a load that never lands ends the wait by its limit)
+            // nothing may be in flight when the CTA exits
+            bulk_wait_all();
             for (int c = max(0, issued - kStages); c < issued; ++c)
                 if (!mbar_wait(&full[c % kStages], (uint32_t)(c / kStages) & 1, p.timeout_ns))
                     report_status(p.status, KDA_ERR_TIMEOUT);
@@ -364,7 +460,8 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             bool ok = STATE_ONLY || chunks == 0 || issue_g(0);
             for (int c = 0; c < chunks && ok; ++c) {
                 const uint32_t s = sb + (c % kStages) * kStageBytes, par = c & 1;
-                ok = wait.one(&bar_state, par);          // S as bf16 and decayed, Y free
+                ok = wait.one(&bar_state, par);          // S as bf16 and decayed
+                if (ok && !STATE_ONLY && c > 0) ok = wait.one(&bar_yfree, par ^ 1);
                 if (!ok) break;
                 tc_fence_after_sync();
                 if (!STATE_ONLY) {
@@ -376,7 +473,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 tc_fence_after_sync();
                 issue_ts(tbase + TM_S, tbase + TM_HI, s + OFF_B, id_up, true);
                 if (!STATE_ONLY) {
-                    ok = wait.one(&bar_scaled, par) && wait.one(&bar_q, par);
+                    ok = wait.one(&bar_q, par);          // Q, and Y scaled
                     if (!ok) break;
                     tc_fence_after_sync();
 #pragma unroll
@@ -393,7 +490,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             if (!mbar_wait(&bar_drain, 0, p.timeout_ns)) report_status(p.status, KDA_ERR_TIMEOUT);
         }
     } else if (warp < kStateWarps) {
-        // ------------------------------------------------------------ state and outputs
+        // ------------------------------------------------------------ state
         const int col = 32 * warp + lane;                                // value column of this lane
         const int half = NH == 2 ? col >> 6 : 0;
         const int head = half ? h1 : h0, pc = NH == 2 ? col & 63 : col;
@@ -417,6 +514,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             if constexpr (STATE_ONLY) {
                 if (seg == 0) store_state(seg_state(unit0 + n_seg - 1), n0, v);
             } else {
+#pragma unroll 2
                 for (int k = 1; k < seg; ++k) {
                     const float d = ex2(p.seg_decay[(size_t)(unit0 + k) * H + head]);
                     const float* l = seg_state(unit0 + k);
@@ -425,6 +523,13 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 }
             }
         };
+        for (int n0 = 0; n0 < N; n0 += 32) {
+            float v[32];
+            load_start(n0, v);
+            if (chunks > 0) tmem_write32(tbase + TM_S + lanes + n0, v);
+            else if (p.ST) store_state(p.ST + s_off, n0, v);             // an empty sequence
+        }
+        tmem_wait_st();
         bool ok = true;
         for (int c = 0; c < chunks && ok; ++c) {
             const uint32_t par = c & 1;
@@ -434,96 +539,43 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             tc_fence_after_sync();
             const float decay = ex2((sc.total[half][0] + sc.total[half][1]) + (sc.total[half][2] + sc.total[half][3]));
             // S: its bf16 copy for this chunk's read-out, then decayed to the chunk's end for the update
-            for (int n0 = 0; n0 < N; n0 += 32) {
-                float v[32];
+#pragma unroll 1
+            for (int n0 = 0; n0 < N; n0 += 64) {
+                float v[64];
                 const uint32_t ta = tbase + TM_S + lanes + n0;
-                if (c == 0) {
-                    load_start(n0, v);
-                } else {
-                    tmem_read32(ta, v);
-                }
+                tmem_read64(ta, v);
                 if (!STATE_ONLY) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8)
+                    for (int i = 0; i < 64; i += 8)
                         *reinterpret_cast<uint4*>(sm + OFF_S + sw128_offset(col, n0 + i, ATOM)) =
                             make_uint4(bf16x2(v[i], v[i + 1]), bf16x2(v[i + 2], v[i + 3]), bf16x2(v[i + 4], v[i + 5]),
                                        bf16x2(v[i + 6], v[i + 7]));
                 }
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= decay;
-                tmem_st16(ta, v);
-                tmem_st16(ta + 16, v + 16);
+                scale_by<64>(v, decay);
+                tmem_write32(ta, v);
+                tmem_write32(ta + 32, v + 32);
             }
             tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before_sync();
             if (!(p.skip_handoff && c == 0)) warp_arrive(&bar_state, lane);
-            if (STATE_ONLY) continue;
-            // Y = C S: row r by 2^{L_r}.  Here a lane is a token.
-            const int r = 32 * warp + lane;
-            float row[NH];
-#pragma unroll
-            for (int i = 0; i < NH; ++i) {
-                float before = 0.f;
-                for (int b = 0; b < quarter; ++b) before += sc.total[i][b];
-                row[i] = ex2(sc.L[i][r] + before);
-            }
-            ok = wait.warp(&bar_cs, par);
-            if (!ok) break;
-            tc_fence_after_sync();
-#pragma unroll
-            for (int cb = 0; cb < kCols; cb += 32) {
-                float v[32];
-                const uint32_t ta = tbase + TM_Y + lanes + cb;
-                const float e = row[NH == 2 ? cb >> 6 : 0];
-                tmem_read32(ta, v);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= e;
-                tmem_st16(ta, v);
-                tmem_st16(ta + 16, v + 16);
-            }
-            tmem_wait_st();
-            tc_fence_before_sync();
-            warp_arrive(&bar_scaled, lane);
-            ok = wait.warp(&bar_px, par);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const int t = tok0 + c * kTok + r;
-            __nv_bfloat16* yr = p.y + ((start + t) * H + h0) * P;        // heads h0 and h0 + 1 are neighbours
-#pragma unroll
-            for (int cb = 0; cb < kCols; cb += 32) {
-                float v[32];
-                const uint32_t ta = tbase + TM_Y + lanes + cb;
-                tmem_read32(ta, v);
-                if (t < len_seq && t < tok0 + len && !(NH == 2 && cb >= 64 && h1 == h0)) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        *reinterpret_cast<uint4*>(yr + cb + i) =
-                            make_uint4(bf16x2(v[i], v[i + 1]), bf16x2(v[i + 2], v[i + 3]), bf16x2(v[i + 4], v[i + 5]),
-                                       bf16x2(v[i + 6], v[i + 7]));
-                }
-            }
-            tc_fence_before_sync();                                      // the next C S overwrites Y
         }
         // the state after the last token (of the sequence; of the segment in the first launch)
-        if (ok && (STATE_ONLY || (last_seg && p.ST))) {
-            if (chunks > 0) ok = wait.warp(&bar_upd, (chunks - 1) & 1);
+        if (ok && chunks > 0 && (STATE_ONLY || (last_seg && p.ST)) && wait.warp(&bar_upd, (chunks - 1) & 1)) {
             tc_fence_after_sync();
-            for (int n0 = 0; n0 < N && ok; n0 += 32) {
-                float v[32];
-                if (chunks > 0) {
-                    tmem_read32(tbase + TM_S + lanes + n0, v);
-                } else {
-                    load_start(n0, v);
-                }
-                store_state(STATE_ONLY ? seg_state(unit) : p.ST + s_off, n0, v);
+#pragma unroll 1
+            for (int n0 = 0; n0 < N; n0 += 64) {
+                float v[64];
+                tmem_read64(tbase + TM_S + lanes + n0, v);
+                float* to = STATE_ONLY ? seg_state(unit) : p.ST + s_off;
+                store_state(to, n0, v);
+                store_state(to, n0 + 32, v + 32);
             }
         }
     } else if (warp < kFirstScore) {
         // ------------------------------------------------------------ decays and weighted x
         const int dw = warp - kFirstDecay;
         const int j = 32 * dw + lane;                                    // a token here
-        const int m = j;                                                 // a value column below
         float rate[NH], bias[NH], raw[NH], total_all[NH];
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
@@ -545,8 +597,16 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             const int n_valid = min(kTok, len - c * kTok);
             float sfx[NH], stp[NH];
 #pragma unroll
+            for (int i = 0; i < NH; ++i) stp[i] = raw[i] + bias[i];
+#pragma unroll 1
+            for (int i = 0; i < NH; ++i) {                               // the heads change places: one copy of the code
+                const float st = j < n_valid ? softplus(stp[0]) : 0.f;
+                const float t0 = stp[NH - 1];
+                stp[NH - 1] = st;
+                if (NH == 2) stp[0] = t0;
+            }
+#pragma unroll
             for (int i = 0; i < NH; ++i) {
-                stp[i] = j < n_valid ? softplus(raw[i] + bias[i]) : 0.f;
                 const float la = stp[i] * rate[i];
                 float incl = la, rev = la;
 #pragma unroll
@@ -557,7 +617,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 }
                 const float after = __shfl_down_sync(0xffffffffu, rev, 1);
                 sfx[i] = lane == 31 ? 0.f : after;                       // tokens after this one in its block
-                sc.L[i][j] = incl;
+                sc.neg[i][j] = -incl;
                 sc.step[i][j] = stp[i];
                 sc.col[i][j] = stp[i] * ex2(sfx[i]);
                 if (lane == 31) sc.total[i][dw] = incl;
@@ -572,7 +632,10 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     if (b > dw) after += sc.total[i][b];
                     all += sc.total[i][b];
                 }
-                sc.w[i][j] = stp[i] * ex2(sfx[i] + after);
+                const float w = stp[i] * ex2(sfx[i] + after);
+                const __nv_bfloat16 w1 = __float2bfloat16_rn(w), w2 = __float2bfloat16_rn(w - __bfloat162float(w1));
+                sc.w1[i][j] = __bfloat16_as_ushort(w1);
+                sc.w2[i][j] = __bfloat16_as_ushort(w2);
                 total_all[i] += all;
             }
             warp_arrive(&bar_scal[c & 1], lane);
@@ -592,32 +655,35 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             ok = named_bar_and(2, 32 * kDecayWarps, ok);
             if (!ok) break;
             tc_fence_after_sync();
-            const float* wv = sc.w[NH == 2 ? m >> 6 : 0];
-            const uint8_t* xt = s + OFF_X + (m >> 6) * ATOM + (m & 7) * 2;
-            const uint32_t chunk16 = (m & 63) >> 3;
-#pragma unroll 2
-            for (int t0 = 0; t0 < kTok; t0 += 16) {
-                uint32_t hi[8], lo[8];
+            // 32 value columns per warp, 32 tokens a step
+            const int half = NH == 2 ? dw >> 1 : 0;
+            const uint32_t* w1 = reinterpret_cast<const uint32_t*>(sc.w1[half]) + (lane & 3);
+            const uint32_t* w2 = reinterpret_cast<const uint32_t*>(sc.w2[half]) + (lane & 3);
+            const uint32_t xa = smem_u32(s) + OFF_X + (dw >> 1) * ATOM + (lane & 7) * 128 +
+                                (((uint32_t)((dw & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
+#pragma unroll 1
+            for (int q4 = 0; q4 < 4; ++q4) {
+                uint32_t hi[2][8], lo[2][8];
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const float4 w4 = *reinterpret_cast<const float4*>(wv + t0 + i);
-                    const float w[4] = {w4.x, w4.y, w4.z, w4.w};
-                    float v[4];
+                for (int k = 0; k < 4; ++k) {
+                    const int tg = 4 * q4 + k;                           // 8 tokens
+                    uint32_t x[4];
+                    ldmatrix4t(xa + tg * 1024, x);
+                    const uint32_t a = w1[4 * tg], b = w2[4 * tg];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int t = t0 + i + k;
-                        const uint32_t u = *reinterpret_cast<const uint16_t*>(xt + t * 128 + ((chunk16 ^ (t & 7)) << 4));
-                        v[k] = __uint_as_float(u << 16) * w[k];
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; k += 2) {
-                        const uint32_t h2 = bf16x2(v[k], v[k + 1]);
-                        hi[(i + k) / 2] = h2;
-                        lo[(i + k) / 2] = bf16x2(v[k] - __uint_as_float(h2 << 16), v[k + 1] - __uint_as_float(h2 & 0xffff0000u));
+                    for (int m = 0; m < 4; ++m) {
+                        const uint32_t h = mul_bf16x2(x[m], a);
+                        const uint32_t rest = fma_bf16x2(x[m], a, h ^ 0x80008000u);
+                        hi[m >> 1][2 * k + (m & 1)] = h;
+                        lo[m >> 1][2 * k + (m & 1)] = fma_bf16x2(x[m], b, rest);
                     }
                 }
-                tmem_st8(tbase + TM_HI + lanes + t0 / 2, hi);
-                tmem_st8(tbase + TM_LO + lanes + t0 / 2, lo);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t at = tbase + lanes + ((uint32_t)(16 * u) << 16) + 16 * q4;
+                    tmem_st_16x128(at + TM_HI, hi[u]);
+                    tmem_st_16x128(at + TM_LO, lo[u]);
+                }
             }
             tmem_wait_st();
             tc_fence_before_sync();
@@ -628,68 +694,112 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             if (NH == 2 && h1 != h0) p.seg_decay[(size_t)unit * H + h1] = total_all[NH - 1];
         }
     } else if (!STATE_ONLY) {
-        // ------------------------------------------------------------ Q: the decayed lower triangle of G
-        const int which = (warp - kFirstScore) >> 2;                     // 16 columns of each 32-column block
+        // ------------------------------------------------------------ Q (the decayed lower triangle of G), outputs
+        const int which = (warp - kFirstScore) >> 2;     // of Q: 16 columns of each 32; of Y: 64 columns
         const int r = 32 * quarter + lane;
-        float skip[NH];
-#pragma unroll
-        for (int i = 0; i < NH; ++i) skip[i] = p.D ? p.D[i ? h1 : h0] : 0.f;
+        const float skip0 = p.D ? p.D[h0] : 0.f, skip1 = p.D ? p.D[h1] : 0.f;
+        const uint32_t yt = tbase + TM_Y + lanes + 64 * which;
         bool ok = true;
         for (int c = 0; c < chunks; ++c) {
             const uint32_t par = c & 1;
             const Scalars& sc = scal[c & 1];
             ok = wait.warp(&bar_scal[c & 1], (c >> 1) & 1) && wait.warp(&bar_g, par);
             tc_fence_after_sync();
-            float gv[4][16];
-            tmem_read4x16(tbase + TM_G + lanes + 16 * which, &gv[0][0]);
-            tc_fence_before_sync();
-            // both warps of these lanes have read G (Q takes its place)
-            ok = named_bar_and(3 + quarter, 64, ok);
-            if (!ok) break;
-            tc_fence_after_sync();
+            float row = 0.f;                             // 2^{L_r}, of this warp's columns of Y
+            {
+                float off[48], diag[16];                 // G: blocks 0 to 2 of 32 columns, and the diagonal's
+                tmem_read3x16(tbase + TM_G + lanes + 16 * which, off, tbase + TM_G + lanes + 32 * quarter + 16 * which, diag);
+                tc_fence_before_sync();
+                // both warps of these lanes have read G (Q takes its place).  They leave only here, together.
+                ok = named_bar_and(3 + quarter, 64, ok);
+                if (!ok) break;
+                tc_fence_after_sync();
+#pragma unroll 1
+                for (int i = 0; i < NH; ++i) {
+                    const uint32_t qt = tbase + TM_G + 64 * i + lanes + 8 * which;
+                    const float* colf = sc.col[i] + 16 * which;
+                    const float lr = -sc.neg[i][r];
+                    float e = lr;                        // sum over the tokens after block b up to r
 #pragma unroll
-            for (int i = 0; i < NH; ++i) {
-                const float lr = sc.L[i][r];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t q[8];
-                    const int j0 = 32 * b + 16 * which;
-                    if (b > quarter) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) q[k] = 0u;
-                    } else if (b < quarter) {
-                        float e = lr;
-                        for (int k = b + 1; k < quarter; ++k) e += sc.total[i][k];
-                        e = ex2(e);
-#pragma unroll
-                        for (int k = 0; k < 16; k += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(&sc.col[i][j0 + k]);
-                            q[k / 2] = bf16x2(gv[b][k] * (e * f.x), gv[b][k + 1] * (e * f.y));
-                            q[k / 2 + 1] = bf16x2(gv[b][k + 2] * (e * f.z), gv[b][k + 3] * (e * f.w));
-                        }
-                    } else {
+                    for (int b = 2; b >= 0; --b) {
+                        if (b >= quarter) continue;
+                        const float ee = ex2(e);
+                        const uint64_t e2 = pair2(ee, ee);
+                        e += sc.total[i][b];
+                        uint32_t q[8];
 #pragma unroll
                         for (int k = 0; k < 16; k += 4) {
-                            const float4 l = *reinterpret_cast<const float4*>(&sc.L[i][j0 + k]);
-                            const float4 s = *reinterpret_cast<const float4*>(&sc.step[i][j0 + k]);
-                            const float lj[4] = {l.x, l.y, l.z, l.w}, sj[4] = {s.x, s.y, s.z, s.w};
-                            float v[4];
-#pragma unroll
-                            for (int d = 0; d < 4; ++d) {
-                                const int j = j0 + k + d;
-                                v[d] = j <= r ? gv[b][k + d] * (ex2(lr - lj[d]) * sj[d]) : 0.f;
-                                if (j == r) v[d] += skip[i];
-                            }
-                            q[k / 2] = bf16x2(v[0], v[1]);
-                            q[k / 2 + 1] = bf16x2(v[2], v[3]);
+                            const float4 f = *reinterpret_cast<const float4*>(colf + 32 * b + k);
+                            const float* gb = off + 16 * b + k;
+                            q[k / 2] = mul2_bf16x2(pair2(gb[0], gb[1]), mul2(e2, pair2(f.x, f.y)));
+                            q[k / 2 + 1] = mul2_bf16x2(pair2(gb[2], gb[3]), mul2(e2, pair2(f.z, f.w)));
                         }
+                        tmem_st8(qt + 16 * b, q);
                     }
-                    tmem_st8(tbase + TM_G + 64 * i + lanes + j0 / 2, q);
+                    if (NH == 1 || i == which) row = ex2(e);
+                    uint32_t q[8];
+                    const float skip = i ? skip1 : skip0;
+                    const float* negd = sc.neg[i] + 32 * quarter + 16 * which;
+                    const float* stepd = sc.step[i] + 32 * quarter + 16 * which;
+                    const int dr = lane - 16 * which;    // the column of the diagonal element
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) {
+                        const float4 l = *reinterpret_cast<const float4*>(negd + k);
+                        const float4 st = *reinterpret_cast<const float4*>(stepd + k);
+                        const float lj[4] = {l.x, l.y, l.z, l.w}, sj[4] = {st.x, st.y, st.z, st.w};
+                        float v[4];
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            const float m = diag[k + d] * (ex2(lr + lj[d]) * sj[d]);
+                            v[d] = k + d < dr ? m : k + d == dr ? m + skip : 0.f;
+                        }
+                        q[k / 2] = bf16x2(v[0], v[1]);
+                        q[k / 2 + 1] = bf16x2(v[2], v[3]);
+                    }
+                    tmem_st8(qt + 16 * quarter, q);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) q[k] = 0u;
+#pragma unroll 1
+                    for (int b = quarter + 1; b < 4; ++b) tmem_st8(qt + 16 * b, q);
                 }
+            }
+            // Y = C S: row r by 2^{L_r}
+            ok = wait.warp(&bar_cs, par);
+            tc_fence_after_sync();
+            {
+                float v[64];
+                tmem_read64(yt, v);
+                scale_by<64>(v, row);
+                tmem_write32(yt, v);
+                tmem_write32(yt + 32, v + 32);
             }
             tmem_wait_st();
             tc_fence_before_sync();
             warp_arrive(&bar_q, lane);
+            // Y, finished: into the chunk's own x tile (all its readers are done), from where the load warp stores it
+            // in whole lines
+            ok = ok && wait.warp(&bar_px, par);
+            tc_fence_after_sync();
+            uint8_t* tile_y = sm + (c % kStages) * kStageBytes + OFF_X + which * ATOM;
+            const bool whole = !p.cu_seqlens || len - c * kTok >= kTok;
+            const int t = c * kTok + r;
+            __nv_bfloat16* yr = p.y + ((start + tok0 + t) * H + h0) * P + 64 * which;    // heads h0, h0 + 1 are neighbours
+            const bool mine = !(NH == 2 && which == 1 && h1 == h0);
+            {
+                float v[64];
+                tmem_read64(yt, v);
+                tc_fence_before_sync();                  // the next C S overwrites Y
+                warp_arrive(&bar_yfree, lane);
+#pragma unroll
+                for (int i = 0; i < 64; i += 8) {
+                    const uint4 o = make_uint4(bf16x2(v[i], v[i + 1]), bf16x2(v[i + 2], v[i + 3]),
+                                               bf16x2(v[i + 4], v[i + 5]), bf16x2(v[i + 6], v[i + 7]));
+                    if (whole) *reinterpret_cast<uint4*>(tile_y + sw128_offset(r, i, ATOM)) = o;
+                    else if (mine && ok && t < len) *reinterpret_cast<uint4*>(yr + i) = o;   // rows past a packed sequence stay
+                }
+            }
+            fence_proxy_async_smem();
+            warp_arrive(&bar_staged, lane);
         }
     }
     tc_fence_before_sync();
@@ -717,18 +827,42 @@ int tiles_of(int H, int G, int P) {
     return G * (P == 64 ? (rep + 1) / 2 : rep);
 }
 
-// Chunks per segment (0: sequences are not cut).
-int segment_chunks(int, long long, int) { return 0; }
+// Chunks per segment (0: sequences are not cut).  With k segments a sequence's tiles run (k - 1)/k of their chunks
+// through the state-only launch and all of them, k times as many CTAs, through the second.  The least of the modelled
+// times is taken, in waves of 148 CTAs and units of a chunk of the full kernel: a state-only chunk costs kStateCost of
+// one, the second launch and the start states about kSplitCost chunks.
+constexpr double kStateCost = 0.55, kSplitCost = 4.0;
+constexpr int kMostSegments = 8;
 
-long long units_of(int n_seq, long long T_total, bool packed, int T, int seg_chunks) {
-    if (seg_chunks == 0) return n_seq;
-    const long long tok = (long long)seg_chunks * kTok;
-    return packed ? n_seq + T_total / tok : (long long)n_seq * ((T + tok - 1) / tok);
+int segment_chunks(int n_seq, long long T_total, int H, int P) {
+    const double ctas = (double)n_seq * (P == 64 ? (H + 1) / 2 : H);
+    const long long chunks = (T_total / n_seq + kTok - 1) / kTok;         // of a sequence, on average
+    auto waves = [](double n) { return (double)(long long)((n + 147.0) / 148.0); };
+    double best = waves(ctas) * (double)chunks;
+    int cut = 0;
+    for (int k = 2; k <= kMostSegments && k <= chunks; ++k) {
+        const long long len = (chunks + k - 1) / k;
+        const double t = len * (waves(ctas * (k - 1)) * kStateCost + waves(ctas * k)) + kSplitCost;
+        if (t < best) {
+            best = t;
+            cut = (int)len;
+        }
+    }
+    return cut;
+}
+
+// Upper bound of the units (segments of sequences) of a call.
+long long units_of(int n_seq, long long T_total, int seg_chunks) {
+    return seg_chunks == 0 ? n_seq : n_seq + T_total / ((long long)seg_chunks * kTok);
+}
+
+size_t workspace_of(long long units, int H, int N, int P) {
+    return (size_t)units * H * ((size_t)N * P + 1) * sizeof(float);
 }
 
 template <int N, int P, bool STATE_ONLY>
-cudaError_t launch_one(const CUtensorMap& mx, const CUtensorMap& mb, const CUtensorMap& mc, const Params& p,
-                       long long units, cudaStream_t s) {
+cudaError_t launch_one(const CUtensorMap& mx, const CUtensorMap& mb, const CUtensorMap& mc, const CUtensorMap& my,
+                       const Params& p, long long units, cudaStream_t s) {
     static std::mutex mu;
     static bool attr_set[64] = {false};
     int dev = 0;
@@ -744,23 +878,29 @@ cudaError_t launch_one(const CUtensorMap& mx, const CUtensorMap& mb, const CUten
     }
     const long long grid = units * p.tiles;
     if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    kda_ssm_tc_kernel<N, P, STATE_ONLY><<<(unsigned)grid, kThreads, SMEM_DYN, s>>>(mx, mb, mc, p);
+    kda_ssm_tc_kernel<N, P, STATE_ONLY><<<(unsigned)grid, kThreads, SMEM_DYN, s>>>(mx, mb, mc, my, p);
     return cudaGetLastError();
 }
 
 template <int N, int P>
-cudaError_t launch_np(const CUtensorMap& mx, const CUtensorMap& mb, const CUtensorMap& mc, const Params& p,
-                     long long units, cudaStream_t s) {
+cudaError_t launch_np(const CUtensorMap& mx, const CUtensorMap& mb, const CUtensorMap& mc, const CUtensorMap& my,
+                      const Params& p, long long units, cudaStream_t s) {
     if (p.seg_chunks > 0) {
-        const cudaError_t e = launch_one<N, P, true>(mx, mb, mc, p, units, s);
+        const cudaError_t e = launch_one<N, P, true>(mx, mb, mc, my, p, units, s);
         if (e != cudaSuccess) return e;
     }
-    return launch_one<N, P, false>(mx, mb, mc, p, units, s);
+    return launch_one<N, P, false>(mx, mb, mc, my, p, units, s);
 }
 
 }  // namespace
 
 bool ssm_tc_supports(const SsmArgs& a) { return a.dtype == KDA_DTYPE_BF16; }
+
+size_t ssm_tc_workspace(int n_seq, long long T_total, int H, int N, int P) {
+    if (T_total == 0) return 0;
+    const int seg_chunks = segment_chunks(n_seq, T_total, H, P);
+    return seg_chunks == 0 ? 0 : workspace_of(units_of(n_seq, T_total, seg_chunks), H, N, P);
+}
 
 cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t s) {
     const int B = a.cu_seqlens ? 1 : a.n_seq;
@@ -770,9 +910,9 @@ cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t s) {
         const size_t bytes = (size_t)a.n_seq * a.H * a.N * a.P * sizeof(float);
         return a.S0 ? cudaMemcpyAsync(a.ST, a.S0, bytes, cudaMemcpyDeviceToDevice, s) : cudaMemsetAsync(a.ST, 0, bytes, s);
     }
-    CUtensorMap mx, mb, mc;
+    CUtensorMap mx, mb, mc, my;
     if (!make_map(&mx, a.x, B, a.T, a.H, a.P, a.ldx) || !make_map(&mb, a.Bm, B, a.T, a.G, a.N, a.ldb) ||
-        !make_map(&mc, a.Cm, B, a.T, a.G, a.N, a.ldc))
+        !make_map(&mc, a.Cm, B, a.T, a.G, a.N, a.ldc) || !make_map(&my, a.y, B, a.T, a.H, a.P, (long long)a.H * a.P))
         return cudaErrorInvalidValue;
     Params p{};
     p.dt = static_cast<const __nv_bfloat16*>(a.dt);
@@ -790,16 +930,20 @@ cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t s) {
     p.G = a.G;
     p.tiles = tiles_of(a.H, a.G, a.P);
     const long long T_total = a.cu_seqlens ? a.T : (long long)a.n_seq * a.T;
-    p.seg_chunks = segment_chunks(a.n_seq, T_total, p.tiles);
-    const long long units = units_of(a.n_seq, T_total, a.cu_seqlens != nullptr, a.T, p.seg_chunks);
-    p.segs = p.seg_chunks > 0 && !a.cu_seqlens ? (int)(units / a.n_seq) : 1;
+    p.seg_chunks = segment_chunks(a.n_seq, T_total, a.H, a.P);
+    long long units = units_of(a.n_seq, T_total, p.seg_chunks);
     p.seg_state = static_cast<float*>(a.workspace);
-    p.seg_decay = p.seg_state ? p.seg_state + (size_t)units * a.H * a.N * a.P : nullptr;
+    p.seg_decay = p.seg_state + (size_t)units * a.H * a.N * a.P;          // units does not grow below
+    p.segs = 1;
+    if (p.seg_chunks > 0 && !a.cu_seqlens) {
+        p.segs = (a.T + p.seg_chunks * kTok - 1) / (p.seg_chunks * kTok);
+        units = (long long)a.n_seq * p.segs;
+    }
     p.status = a.status;
     p.timeout_ns = a.timeout_ns;
     p.skip_handoff = a.skip_handoff;
-    if (a.N == 128) return a.P == 128 ? launch_np<128, 128>(mx, mb, mc, p, units, s) : launch_np<128, 64>(mx, mb, mc, p, units, s);
-    return a.P == 128 ? launch_np<64, 128>(mx, mb, mc, p, units, s) : launch_np<64, 64>(mx, mb, mc, p, units, s);
+    if (a.N == 128) return a.P == 128 ? launch_np<128, 128>(mx, mb, mc, my, p, units, s) : launch_np<128, 64>(mx, mb, mc, my, p, units, s);
+    return a.P == 128 ? launch_np<64, 128>(mx, mb, mc, my, p, units, s) : launch_np<64, 64>(mx, mb, mc, my, p, units, s);
 }
 
 }  // namespace kda

@@ -67,14 +67,15 @@ def scan_bounds(y, ya, Sa, T, N, dtype, impl):
 
     fp32 arithmetic: a token's decay, time step and products are each off by a few 2^-24, and a term stays in
     the state for at most T tokens, so 8 T + N steps of 2^-24 of its magnitude cover it.  The tensor-core
-    kernel reads the state and the decayed scores as bf16 operands (2^-8 of each term of y) and adds to the
-    state s_j x_j e^(..) as a sum of two bf16 values (2^-16 of each term)."""
+    kernel reads the state and the decayed scores as bf16 operands (2^-8 of each term of y).  To the state it
+    adds x w, w = s_j e^(..), as hi + lo: w is taken as two bf16 values (off by 2^-8 of the second, which is at
+    most 2^-8 w), and lo, at most 2 * 2^-8 of the term, is rounded to bf16: (1 + 2) * 2^-16 of each term."""
     f32 = (8 * T + N + 64) * 2.0 ** -24
     by = HALF[dtype] * np.abs(y) + f32 * ya
     bS = f32 * Sa
     if impl == "tcgen05":
         by = by + 1.01 * 2.0 ** -8 * ya
-        bS = bS + 2.0 ** -16 * Sa
+        bS = bS + 3 * 2.0 ** -16 * Sa
     return by + 1e-30, bS + 1e-30
 
 

@@ -284,6 +284,74 @@ def test_on_a_stream_and_in_a_graph(dtype, impl):
         assert torch.equal(y0, yg) and torch.equal(S0, Sg)
 
 
+LONG = [(1, 1700, 1, 1, 128, 128), (1, 2048, 3, 1, 64, 64), (2, 1281, 2, 1, 128, 64), (1, 4097, 2, 2, 64, 128)]
+
+
+@pytest.mark.parametrize("B,T,H,G,N,P", LONG)
+def test_long_prompts_of_few_heads_ask_for_a_workspace(L, B, T, H, G, N, P):
+    need = kda.ssm_workspace_bytes(B, B * T, H, N, P)
+    assert need >= 2 * B * H * N * P * 4 and need % 4 == 0
+    assert kda.ssm_workspace_bytes(B, B * T, H, N, P, torch.float32) == 0
+    assert kda.ssm_workspace_bytes(B, B * T, H, N, P, impl="simt") == 0
+    assert kda.ssm_workspace_bytes(4, 4 * 8192, 96, 128, 128) == 0           # enough heads: no segments
+    f = lambda **k: call(L, B=B, T=T, H=H, G=G, N=N, P=P, **k)  # noqa: E731
+    assert f(ws=None) == INVALID and f(ws_bytes=need - 1) == INVALID
+    assert f(ws=AT["ws"] + 8) == MISALIGNED
+    assert f(ws=AT["ST"]) == INVALID and f(ws=AT["x"] + 64) == INVALID
+
+
+@gpu
+@pytest.mark.parametrize("B,T,H,G,N,P", LONG)
+def test_segments(B, T, H, G, N, P):
+    """Prompts cut into segments: against fp64, in place, and packed with shorter ones."""
+    c = case((B, T), H, G, N, P, "bf16", seed=T, rate=1.5)
+    y, S = kda.kda_ssm_forward(**c)
+    assert kda.kda_get_device_status() == 0
+    for b in range(B):
+        check(y[b], S[b], c, b, b, "bf16", "tcgen05")
+    held = c["S0"].clone()
+    y2, S2 = kda.kda_ssm_forward(**{**c, "S0": held}, S_T=held)
+    assert torch.equal(y, y2) and torch.equal(S, S2)
+    ws = torch.full((kda.ssm_workspace_bytes(B, B * T, H, N, P),), 255, dtype=torch.uint8, device="cuda")   # NaN
+    y3, S3 = kda.kda_ssm_forward(**c, workspace=ws)
+    assert torch.equal(y, y3) and torch.equal(S, S3)
+
+
+@gpu
+def test_segments_packed():
+    lengths, lead, tail = [3000, 0, 129, 2500, 1500], 3, 5
+    T, H, G, N, P = lead + sum(lengths) + tail, 2, 1, 128, 64
+    c = case((T,), H, G, N, P, "bf16", seed=9, states=len(lengths), rate=1.5)
+    assert kda.ssm_workspace_bytes(len(lengths), T, H, N, P) > 0
+    for k in ("x", "dt", "Bm", "Cm"):
+        c[k][:lead] = float("nan")
+        c[k][T - tail:] = float("inf")
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]) + lead, dtype=torch.int32, device="cuda")
+    y = torch.full((T, H, P), 7.0, dtype=torch.bfloat16, device="cuda")
+    held = c["S0"].clone()
+    y, S = kda.kda_ssm_forward_varlen(**{**c, "S0": held}, cu_seqlens=cu, y=y, S_T=held)
+    assert kda.kda_get_device_status() == 0
+    at = lead
+    for n, k in enumerate(lengths):
+        check(y[at:at + k], S[n], c, slice(at, at + k), n, "bf16", "tcgen05")
+        at += k
+    assert bool((y[:lead] == 7).all()) and bool((y[T - tail:] == 7).all())
+
+
+@gpu
+def test_a_wait_that_runs_out_is_reported():
+    c = case((1, 300), 2, 1, 128, 64, "bf16", seed=8)
+    want = kda.kda_ssm_forward(**c)
+    kda.kda_debug_set_wait_fault(1, 20_000_000)
+    try:
+        kda.kda_ssm_forward(**c)
+        assert kda.kda_get_device_status() == STATUS["KDA_ERR_TIMEOUT"]
+    finally:
+        kda.kda_debug_set_wait_fault(0)
+    y, S = kda.kda_ssm_forward(**c)
+    assert kda.kda_get_device_status() == 0 and torch.equal(y, want[0]) and torch.equal(S, want[1])
+
+
 @gpu
 def test_a_layer_as_it_is_served():
     """Convolution, scan, a fork of both states to three continuations, single tokens, compaction: each
