@@ -2,10 +2,13 @@
 // sequence after its last W-1 inputs (the state), for prompts and for single tokens.
 //
 // Bound by HBM: every element of x is read and every element of y written once for W multiply-adds
-// and one sigmoid.  Lanes run along the channels with 16-byte vectors.  In the prompt kernel a thread
-// carries the last W-1 inputs of its channels in registers down a strip of tokens, so x is read once
-// except for the W-1 rows above each strip (mostly L2 hits: the strip above is in flight), and eight
-// rows are loaded before the first is used.
+// and one sigmoid.  In the prompt kernel a thread carries the last W-1 inputs of its four channels in
+// registers down a strip of tokens, so x is read once except for the W-1 rows above each strip (mostly
+// L2 hits: the strip above is in flight), and loads 16 (fp32: 8) rows before it uses the first.  In bf16
+// the arithmetic is nearly as long as the traffic: the f32x2 instructions take two channels at once,
+// and four channels a thread keep registers low enough for five blocks an SM.  One B200, 16384 x 12288
+// bf16 with SiLU: 150 us (0.82 of the measured copy rate; 127 us without the activation); eight
+// channels a thread with 16-byte loads 159 us, scalar arithmetic 222 us; fp32 254 us (0.97).
 //
 // The first W-1 tokens of a sequence, which need the state, and the state after its last token belong
 // to blocks of their own, one per sequence and channel range: those read everything before they write
@@ -16,47 +19,86 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kAhead = 8;       // rows in flight per thread
 
+constexpr int kVec = 4;          // channels per thread
+
+// a thread's channels of one row, as they lie in memory
 template <typename T>
-struct Vec {
-    static constexpr int n = 16 / sizeof(T);
+struct Raw;
+template <>
+struct Raw<float> {
+    using type = uint4;
+    static constexpr int ahead = 8, blocks = 1;      // rows in flight per thread, blocks per SM asked of the compiler
+};
+template <>
+struct Raw<__nv_bfloat16> {
+    using type = uint2;
+    static constexpr int ahead = 16, blocks = 5;
 };
 
-__device__ __forceinline__ void unpack(const uint4& r, float (&f)[4]) {
-    f[0] = __uint_as_float(r.x); f[1] = __uint_as_float(r.y); f[2] = __uint_as_float(r.z); f[3] = __uint_as_float(r.w);
+// Channels go in pairs, two fp32 lanes of one 64-bit register (the f32x2 instructions).
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
-__device__ __forceinline__ void unpack(const uint4& r, float (&f)[8]) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+__device__ __forceinline__ float2 split2(uint64_t p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+    return f;
 }
-__device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
-__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&p);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack(const uint4& r, uint64_t (&f)[2]) {
+    f[0] = pair2(__uint_as_float(r.x), __uint_as_float(r.y));
+    f[1] = pair2(__uint_as_float(r.z), __uint_as_float(r.w));
+}
+__device__ __forceinline__ void unpack(const uint2& r, uint64_t (&f)[2]) {
+    f[0] = pair2(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u));
+    f[1] = pair2(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
+}
+__device__ __forceinline__ void pack(const uint64_t (&f)[2], uint4& r) {
+    const float2 a = split2(f[0]), b = split2(f[1]);
+    r = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+}
+__device__ __forceinline__ void pack(const uint64_t (&f)[2], uint2& r) {
+    const float2 a = split2(f[0]), b = split2(f[1]);
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a.x, a.y), q = __floats2bfloat162_rn(b.x, b.y);
+    r = make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
 }
 
-// v sigmoid(v).  bf16 outputs (relative step 2^-8) take the approximate exponential and division
-// (relative error about 2^-21), fp32 outputs the accurate ones.
-__device__ __forceinline__ float silu(float v, const __nv_bfloat16*) { return __fdividef(v, 1.f + __expf(-v)); }
-__device__ __forceinline__ float silu(float v, const float*) { return v / (1.f + expf(-v)); }
+// v / (1 + 2^(-v log2 e)), both lanes: the hardware exponential and reciprocal, each off by about 2^-22, and the
+// exponent's rounding, 2^-24 of it (all far below a bf16 step; for fp32 a few units in the last place)
+__device__ __forceinline__ uint64_t silu2(uint64_t v) {
+    const float2 a = split2(mul2(v, pair2(-1.4426950408889634f, -1.4426950408889634f)));
+    float ex, ey, rx, ry;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ex) : "f"(a.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ey) : "f"(a.y));
+    const float2 d = split2(add2(pair2(ex, ey), pair2(1.f, 1.f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rx) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ry) : "f"(d.y));
+    return mul2(v, pair2(rx, ry));
+}
 
 // Weights and bias of a thread's channels, and the filter applied to a window of inputs.
 template <typename T, int W>
 struct Filter {
-    static constexpr int V = Vec<T>::n;
-    float w[W][V], b[V];
+    static constexpr int V = kVec, H = V / 2;
+    using R = typename Raw<T>::type;
+    uint64_t w[W][H], b[H];
     bool act;
 
     __device__ __forceinline__ void load(const T* weight, const T* bias, int c, bool silu_on) {
@@ -64,62 +106,67 @@ struct Filter {
         float flat[W * V];
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            float t[V];
-            unpack(__ldg(reinterpret_cast<const uint4*>(weight + (size_t)c * W) + i), t);
+            uint64_t t[H];
+            unpack(__ldg(reinterpret_cast<const R*>(weight + (size_t)c * W) + i), t);
 #pragma unroll
-            for (int j = 0; j < V; ++j) flat[i * V + j] = t[j];
+            for (int j = 0; j < H; ++j) {
+                const float2 f = split2(t[j]);
+                flat[i * V + 2 * j] = f.x;
+                flat[i * V + 2 * j + 1] = f.y;
+            }
         }
 #pragma unroll
         for (int i = 0; i < W; ++i)
 #pragma unroll
-            for (int j = 0; j < V; ++j) w[i][j] = flat[j * W + i];
+            for (int j = 0; j < H; ++j) w[i][j] = pair2(flat[2 * j * W + i], flat[(2 * j + 1) * W + i]);
         if (bias) {
-            unpack(__ldg(reinterpret_cast<const uint4*>(bias + c)), b);
+            unpack(__ldg(reinterpret_cast<const R*>(bias + c)), b);
         } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) b[j] = 0.f;
+            for (int j = 0; j < H; ++j) b[j] = 0;
         }
         act = silu_on;
     }
     // win: the W-1 inputs before `u`, oldest first; shifted by one afterwards
-    __device__ __forceinline__ uint4 apply(float (&win)[W - 1][V], const uint4& u) const {
-        float cur[V], out[V];
+    __device__ __forceinline__ R apply(uint64_t (&win)[W - 1][H], const R& u) const {
+        uint64_t cur[H], out[H];
         unpack(u, cur);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float a = b[j];
+        for (int j = 0; j < H; ++j) {
+            uint64_t a = b[j];
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) a = fmaf(w[i][j], win[i][j], a);
-            out[j] = fmaf(w[W - 1][j], cur[j], a);
+            for (int i = 0; i < W - 1; ++i) a = fma2(w[i][j], win[i][j], a);
+            out[j] = fma2(w[W - 1][j], cur[j], a);
         }
-        push(win, cur);
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+#pragma unroll
+            for (int i = 0; i + 1 < W - 1; ++i) win[i][j] = win[i + 1][j];
+            win[W - 2][j] = cur[j];
+        }
         if (act) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) out[j] = silu(out[j], static_cast<const T*>(nullptr));
+            for (int j = 0; j < H; ++j) out[j] = silu2(out[j]);
         }
-        return pack(out);
-    }
-    __device__ __forceinline__ static void push(float (&win)[W - 1][V], const float (&cur)[V]) {
-#pragma unroll
-        for (int i = 0; i + 1 < W - 1; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) win[i][j] = win[i + 1][j];
-#pragma unroll
-        for (int j = 0; j < V; ++j) win[W - 2][j] = cur[j];
+        R r;
+        pack(out, r);
+        return r;
     }
 };
 
 template <typename T>
-__device__ __forceinline__ uint4 load_row(const T* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ typename Raw<T>::type load_row(const T* p) {
+    return __ldg(reinterpret_cast<const typename Raw<T>::type*>(p));
+}
 
 // Grid: channel ranges fastest, then one block per sequence (start and state), then the strips.
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, Raw<T>::blocks)
 kda_short_conv_kernel(const T* __restrict__ x, const T* __restrict__ weight, const T* __restrict__ bias,
                       const T* state, T* __restrict__ y, T* state_out, const int* __restrict__ cu_seqlens,
                       int n_seq, int T_all, int C, long long ldx, long long ldy, int act, int strip, int n_cb,
                       int strips_per_seq, int* status) {
-    constexpr int V = Vec<T>::n;
+    constexpr int V = kVec;
     const int cb = blockIdx.x % n_cb;
     const int part = blockIdx.x / n_cb;
     bool valid = true;
@@ -131,8 +178,9 @@ kda_short_conv_kernel(const T* __restrict__ x, const T* __restrict__ weight, con
     if (c >= C) return;
     Filter<T, W> f;
     f.load(weight, bias, c, act != 0);
-    float win[W - 1][V];
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint64_t win[W - 1][V / 2];
+    using R = typename Raw<T>::type;
+    const R zero{};
 
     if (part < n_seq) {
         // the first W-1 tokens of sequence `part`, then the state after its last
@@ -144,17 +192,17 @@ kda_short_conv_kernel(const T* __restrict__ x, const T* __restrict__ weight, con
         }
         const T* xs = x + base * ldx + c;
         const T* st = state ? state + (size_t)part * (W - 1) * C + c : nullptr;
-        uint4 raw[W - 1], last[W - 1];
+        R raw[W - 1], last[W - 1];
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) {
-            raw[i] = st ? *reinterpret_cast<const uint4*>(st + (size_t)i * C) : zero;
+            raw[i] = st ? *reinterpret_cast<const R*>(st + (size_t)i * C) : zero;
             unpack(raw[i], win[i]);
         }
 #pragma unroll
         for (int i = 0; i < W - 1; ++i)
             if (i < len) {
-                const uint4 r = f.apply(win, load_row(xs + (size_t)i * ldx));
-                *reinterpret_cast<uint4*>(y + (base + i) * ldy + c) = r;
+                const R r = f.apply(win, load_row(xs + (size_t)i * ldx));
+                *reinterpret_cast<R*>(y + (base + i) * ldy + c) = r;
             }
         if (!state_out) return;
         // entry i of the new state is input len - (W-1) + i: of x, or (shorter sequences) of the state
@@ -172,7 +220,7 @@ kda_short_conv_kernel(const T* __restrict__ x, const T* __restrict__ weight, con
         }
 #pragma unroll
         for (int i = 0; i < W - 1; ++i)
-            *reinterpret_cast<uint4*>(state_out + ((size_t)part * (W - 1) + i) * C + c) = last[i];
+            *reinterpret_cast<R*>(state_out + ((size_t)part * (W - 1) + i) * C + c) = last[i];
         return;
     }
 
@@ -207,23 +255,34 @@ kda_short_conv_kernel(const T* __restrict__ x, const T* __restrict__ weight, con
         const int t = t0 - (W - 1) + i;
         unpack(t >= 0 ? load_row(xs + (size_t)t * ldx) : zero, win[i]);
     }
-    for (int tb = t0; tb < t1; tb += kAhead) {
-        uint4 raw[kAhead];
+    constexpr int kAhead = Raw<T>::ahead, kFew = 4;
+    for (int tb = t0; tb < t1;) {
+        if (tb - start >= W - 1 && tb + kAhead <= min(t1, end)) {
+            R raw[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) raw[i] = tb + i < t1 ? load_row(xs + (size_t)(tb + i) * ldx) : zero;
+            for (int i = 0; i < kAhead; ++i) raw[i] = load_row(xs + (size_t)(tb + i) * ldx);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int t = tb + i;
-            if (t < t1) {
-                while (t >= end) {      // packed only: the next sequence (t < cu[n_seq], so there is one)
-                    ++n;
-                    start = end;
-                    end = __ldg(cu_seqlens + n + 1);
-                }
-                const uint4 r = f.apply(win, raw[i]);
-                if (t - start >= W - 1) *reinterpret_cast<uint4*>(ys + (size_t)t * ldy) = r;
-            }
+            for (int i = 0; i < kAhead; ++i) *reinterpret_cast<R*>(ys + (size_t)(tb + i) * ldy) = f.apply(win, raw[i]);
+            tb += kAhead;
+            continue;
         }
+        // a sequence starts or ends in these rows, or the strip does: a few at a time
+        R raw[kFew];
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) raw[i] = tb + i < t1 ? load_row(xs + (size_t)(tb + i) * ldx) : zero;
+#pragma unroll 1
+        for (int t = tb; t < min(tb + kFew, t1); ++t) {
+            while (t >= end) {          // packed only: the next sequence (t < cu[n_seq], so there is one)
+                ++n;
+                start = end;
+                end = __ldg(cu_seqlens + n + 1);
+            }
+            const R r = f.apply(win, raw[0]);
+            if (t - start >= W - 1) *reinterpret_cast<R*>(ys + (size_t)t * ldy) = r;
+#pragma unroll
+            for (int i = 0; i + 1 < kFew; ++i) raw[i] = raw[i + 1];
+        }
+        tb += kFew;
     }
 }
 
@@ -234,7 +293,8 @@ __global__ void __launch_bounds__(kThreads)
 kda_short_conv_step_kernel(const T* __restrict__ x, const T* __restrict__ weight, const T* __restrict__ bias, T* state,
                            T* __restrict__ y, int B, int C, long long ldx, long long ldy, int act, int n_cb,
                            int seqs, const int* __restrict__ slots, int n_slots, int* status) {
-    constexpr int V = Vec<T>::n;
+    using R = typename Raw<T>::type;
+    constexpr int V = kVec;
     const int cb = blockIdx.x % n_cb;
     const int b0 = (blockIdx.x / n_cb) * seqs;
     const int c = (cb * kThreads + (int)threadIdx.x) * V;
@@ -243,7 +303,7 @@ kda_short_conv_step_kernel(const T* __restrict__ x, const T* __restrict__ weight
     f.load(weight, bias, c, act != 0);
     const int b1 = min(b0 + seqs, B);
     for (int bb = b0; bb < b1; bb += kStepSeqs) {
-        uint4 u[kStepSeqs], raw[kStepSeqs][W - 1];
+        R u[kStepSeqs], raw[kStepSeqs][W - 1];
         long long at[kStepSeqs];
 #pragma unroll
         for (int k = 0; k < kStepSeqs; ++k) {
@@ -260,31 +320,31 @@ kda_short_conv_step_kernel(const T* __restrict__ x, const T* __restrict__ weight
                 u[k] = load_row(x + (size_t)b * ldx + c);
 #pragma unroll
                 for (int i = 0; i < W - 1; ++i)
-                    raw[k][i] = *reinterpret_cast<const uint4*>(state + ((size_t)at[k] * (W - 1) + i) * C + c);
+                    raw[k][i] = *reinterpret_cast<const R*>(state + ((size_t)at[k] * (W - 1) + i) * C + c);
             }
         }
 #pragma unroll
         for (int k = 0; k < kStepSeqs; ++k) {
             if (at[k] < 0) continue;
-            float win[W - 1][V];
+            uint64_t win[W - 1][V / 2];
 #pragma unroll
             for (int i = 0; i < W - 1; ++i) unpack(raw[k][i], win[i]);
-            *reinterpret_cast<uint4*>(y + (size_t)(bb + k) * ldy + c) = f.apply(win, u[k]);
+            *reinterpret_cast<R*>(y + (size_t)(bb + k) * ldy + c) = f.apply(win, u[k]);
             T* st = state + (size_t)at[k] * (W - 1) * C + c;
 #pragma unroll
-            for (int i = 0; i + 1 < W - 1; ++i) *reinterpret_cast<uint4*>(st + (size_t)i * C) = raw[k][i + 1];
-            *reinterpret_cast<uint4*>(st + (size_t)(W - 2) * C) = u[k];
+            for (int i = 0; i + 1 < W - 1; ++i) *reinterpret_cast<R*>(st + (size_t)i * C) = raw[k][i + 1];
+            *reinterpret_cast<R*>(st + (size_t)(W - 2) * C) = u[k];
         }
     }
 }
 
 template <typename T, int W>
 cudaError_t launch_prompt(const ConvArgs& a, cudaStream_t s) {
-    constexpr int V = Vec<T>::n;
+    constexpr int V = kVec;
     const int n_cb = (a.C / V + kThreads - 1) / kThreads;
     // a short strip gives small problems enough blocks, a long one re-reads fewer rows above it
     const long long tokens = a.cu_seqlens ? a.T : (long long)a.n_seq * a.T;
-    int strip = 8;
+    int strip = Raw<T>::ahead;
     while (strip < 64 && tokens / (2 * strip) * n_cb >= 148 * 16) strip *= 2;
     const int per_seq = (a.T + strip - 1) / strip;
     const long long strips = a.cu_seqlens ? per_seq : (long long)a.n_seq * per_seq;
@@ -299,7 +359,7 @@ cudaError_t launch_prompt(const ConvArgs& a, cudaStream_t s) {
 
 template <typename T, int W>
 cudaError_t launch_step(const ConvArgs& a, cudaStream_t s) {
-    constexpr int V = Vec<T>::n;
+    constexpr int V = kVec;
     const int n_cb = (a.C / V + kThreads - 1) / kThreads;
     int seqs = kStepSeqs;    // more sequences per block share the weights, once there are blocks enough
     while (seqs < 8 && (long long)a.n_seq / (2 * seqs) * n_cb >= 148 * 8) seqs *= 2;
