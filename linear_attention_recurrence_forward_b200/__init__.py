@@ -524,21 +524,33 @@ def kda_output_correct(C, S_in, o_in, *, out=None, stream=None):
 # ------------------------------------------------------------------ short convolution, scan, pools
 
 
+_SAME_DEVICE = contextlib.nullcontext()
+
+
 def _on_device(dev: torch.device):
     """The device of the tensors made current for a call (nothing to do when it is already)."""
     if dev.type != "cuda":
         raise ValueError(f"expected CUDA tensors, got {dev}")
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+    if dev.index == torch.cuda.current_device():
+        return _SAME_DEVICE
     return torch.cuda.device(dev)
 
 
-def _empty(shape, dtype, dev, stream) -> torch.Tensor:
-    """An output or workspace in memory of the stream the call runs on."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+def _stream_on(dev: torch.device, stream) -> Optional[int]:
+    """The handle of `stream`, or of the device's current stream (read without making a Stream object, which
+    would cost as much as the launch)."""
+    return (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream) or None
+
+
+def _empty(shape, dtype, dev, stream, like=None) -> torch.Tensor:
+    """An output or workspace in memory of the stream the call runs on; `like`: a tensor that may have its shape,
+    dtype and a dense layout (the shortest way to it)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=dev)
+    if like is not None and like.dtype == dtype and like.shape == shape and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _rows(t, name: str, lead, row, dtype, device) -> int:
@@ -595,7 +607,7 @@ def _conv_common(x, lead, weight, bias, y, activation, stream):
     b = _vector(bias, "bias", C, dt, dev)
     ldx = _rows(x, "x", lead, (C,), dt, dev)
     if y is None:
-        y, ldy = _empty(lead + (C,), dt, dev, stream), C
+        y, ldy = _empty(lead + (C,), dt, dev, stream, x), C
     else:
         ldy = _rows(y, "y", lead, (C,), dt, dev)
     return C, W, y, ldx, ldy, weight.data_ptr(), b, ACTIVATION[activation]
@@ -614,10 +626,10 @@ def kda_short_conv(x, weight, bias=None, state=None, *, activation="silu", y=Non
     if state_out is not None:
         _check(state_out, "state_out", (B, W - 1, C), dt, dev)
     elif return_state:
-        state_out = _empty((B, W - 1, C), dt, dev, stream)
+        state_out = _empty((B, W - 1, C), dt, dev, stream, state)
     with _on_device(dev):
         rc = lib().kda_short_conv(x.data_ptr(), w, b, _ptr(state), y.data_ptr(), _ptr(state_out), B, T, C, W, ldx,
-                                  ldy, act, DTYPE[dt], _stream_handle(stream))
+                                  ldy, act, DTYPE[dt], _stream_on(dev, stream))
     if rc != 0:
         raise KdaError("kda_short_conv", rc)
     return y, state_out
@@ -637,11 +649,11 @@ def kda_short_conv_varlen(x, weight, cu_seqlens, bias=None, state=None, *, activ
     if state_out is not None:
         _check(state_out, "state_out", (N, W - 1, C), dt, dev)
     elif return_state:
-        state_out = _empty((N, W - 1, C), dt, dev, stream)
+        state_out = _empty((N, W - 1, C), dt, dev, stream, state)
     with _on_device(dev):
         rc = lib().kda_short_conv_varlen(x.data_ptr(), w, b, cu_seqlens.data_ptr(), _ptr(state), y.data_ptr(),
                                          _ptr(state_out), N, T_total, C, W, ldx, ldy, act, DTYPE[dt],
-                                         _stream_handle(stream))
+                                         _stream_on(dev, stream))
     if rc != 0:
         raise KdaError("kda_short_conv_varlen", rc)
     return y, state_out
@@ -655,7 +667,7 @@ def kda_short_conv_step(x, weight, state, bias=None, *, activation="silu", y=Non
     _check(state, "state", (B, W - 1, C), dt, dev)
     with _on_device(dev):
         rc = lib().kda_short_conv_step(x.data_ptr(), w, b, state.data_ptr(), y.data_ptr(), B, C, W, ldx, ldy, act,
-                                       DTYPE[dt], _stream_handle(stream))
+                                       DTYPE[dt], _stream_on(dev, stream))
     if rc != 0:
         raise KdaError("kda_short_conv_step", rc)
     return y
@@ -672,7 +684,7 @@ def kda_short_conv_step_paged(x, weight, state_pool, slots, bias=None, *, activa
     _check(slots, "slots", (B,), torch.int32, dev)
     with _on_device(dev):
         rc = lib().kda_short_conv_step_paged(x.data_ptr(), w, b, state_pool.data_ptr(), n_slots, slots.data_ptr(),
-                                             y.data_ptr(), B, C, W, ldx, ldy, act, DTYPE[dt], _stream_handle(stream))
+                                             y.data_ptr(), B, C, W, ldx, ldy, act, DTYPE[dt], _stream_on(dev, stream))
     if rc != 0:
         raise KdaError("kda_short_conv_step_paged", rc)
     return y
@@ -689,7 +701,7 @@ def _ssm_common(x, dt, A, Bm, Cm, D, dt_bias, lead, y, stream):
     _check(A, "A", (H,), torch.float32, dev)
     d, bias = _vector(D, "D", H, torch.float32, dev), _vector(dt_bias, "dt_bias", H, torch.float32, dev)
     if y is None:
-        y = _empty(lead + (H, P), ty, dev, stream)
+        y = _empty(lead + (H, P), ty, dev, stream, x)
     else:
         _check(y, "y", lead + (H, P), ty, dev)
     return H, G, N, P, y, lds, d, bias
@@ -728,12 +740,12 @@ def kda_ssm_forward(x, dt, A, Bm, Cm, D=None, dt_bias=None, S0=None, *, y=None, 
     if S_T is not None:
         _check(S_T, "S_T", (B, H, N, P), torch.float32, dev)
     elif return_state:
-        S_T = _empty((B, H, N, P), torch.float32, dev, stream)
+        S_T = _empty((B, H, N, P), torch.float32, dev, stream, S0)
     with _on_device(dev):
         workspace = _ssm_workspace(workspace, B, B * T, H, N, P, ty, dev, impl, stream)
         rc = lib().kda_ssm_forward(x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), d, bias,
                                    _ptr(S0), y.data_ptr(), _ptr(S_T), B, T, H, G, N, P, *lds, DTYPE[ty], IMPL[impl],
-                                   _ptr(workspace), _nbytes(workspace), _stream_handle(stream))
+                                   _ptr(workspace), _nbytes(workspace), _stream_on(dev, stream))
     if rc != 0:
         raise KdaError("kda_ssm_forward", rc)
     return y, S_T
@@ -754,13 +766,13 @@ def kda_ssm_forward_varlen(x, dt, A, Bm, Cm, cu_seqlens, D=None, dt_bias=None, S
     if S_T is not None:
         _check(S_T, "S_T", (n_seq, H, N, P), torch.float32, dev)
     elif return_state:
-        S_T = _empty((n_seq, H, N, P), torch.float32, dev, stream)
+        S_T = _empty((n_seq, H, N, P), torch.float32, dev, stream, S0)
     with _on_device(dev):
         workspace = _ssm_workspace(workspace, n_seq, T_total, H, N, P, ty, dev, impl, stream)
         rc = lib().kda_ssm_forward_varlen(x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(),
                                           cu_seqlens.data_ptr(), d, bias, _ptr(S0), y.data_ptr(), _ptr(S_T), n_seq,
                                           T_total, H, G, N, P, *lds, DTYPE[ty], IMPL[impl], _ptr(workspace),
-                                          _nbytes(workspace), _stream_handle(stream))
+                                          _nbytes(workspace), _stream_on(dev, stream))
     if rc != 0:
         raise KdaError("kda_ssm_forward_varlen", rc)
     return y, S_T
@@ -776,7 +788,7 @@ def kda_ssm_decode_step(x, dt, A, Bm, Cm, S, D=None, dt_bias=None, *, y=None, st
     with _on_device(dev):
         rc = lib().kda_ssm_decode_step(x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), d,
                                        bias, S.data_ptr(), y.data_ptr(), B, H, G, N, P, *lds, DTYPE[ty],
-                                       _stream_handle(stream))
+                                       _stream_on(dev, stream))
     if rc != 0:
         raise KdaError("kda_ssm_decode_step", rc)
     return y
@@ -794,7 +806,7 @@ def kda_ssm_decode_step_paged(x, dt, A, Bm, Cm, S_pool, slots, D=None, dt_bias=N
     with _on_device(dev):
         rc = lib().kda_ssm_decode_step_paged(x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(),
                                              d, bias, S_pool.data_ptr(), n_slots, slots.data_ptr(), y.data_ptr(), B,
-                                             H, G, N, P, *lds, DTYPE[ty], _stream_handle(stream))
+                                             H, G, N, P, *lds, DTYPE[ty], _stream_on(dev, stream))
     if rc != 0:
         raise KdaError("kda_ssm_decode_step_paged", rc)
     return y
@@ -812,11 +824,16 @@ def _pools(pools, name: str, device=None, beside=None):
     if device is None:
         device = pools[0].device
     for i, t in enumerate(pools):
-        shape, stride, es = t.shape, t.stride(), t.element_size()
+        shape = t.shape
         if t.device != device:
             raise ValueError(f"{name}: a pool is on {t.device}, expected {device}")
         if len(shape) < 2 or shape[0] != n_slots:
             raise ValueError(f"{name}: pools have shape [{n_slots}, ...], got {tuple(shape)}")
+        if t.is_contiguous() and (beside is None or beside[i].is_contiguous()):
+            slot = t.nbytes // n_slots if n_slots else 0
+            flat += (t.data_ptr(), slot, 1, 0, slot)
+            continue
+        stride, es = t.stride(), t.element_size()
         run, d = 1, len(shape) - 1
         last = 1 if beside is not None and len(shape) > 2 and not beside[i].is_contiguous() else 0
         while d > last and (stride[d] == run or shape[d] == 1):
@@ -853,7 +870,7 @@ def kda_pool_copy(pools, src, dst, *, src_pools=None, stream=None) -> None:
     _check(dst, "dst", (n,), torch.int32, dev)
     with _on_device(dev):
         rc = lib().kda_pool_copy(to, frm, len(pools), n_dst, n_src, src.data_ptr(), dst.data_ptr(), n,
-                                 _stream_handle(stream))
+                                 _stream_on(dev, stream))
     if rc != 0:
         raise KdaError("kda_pool_copy", rc)
 
@@ -864,7 +881,7 @@ def kda_pool_clear(pools, slots, *, stream=None) -> None:
     n = slots.shape[0]
     _check(slots, "slots", (n,), torch.int32, dev)
     with _on_device(dev):
-        rc = lib().kda_pool_clear(to, len(pools), n_slots, slots.data_ptr(), n, _stream_handle(stream))
+        rc = lib().kda_pool_clear(to, len(pools), n_slots, slots.data_ptr(), n, _stream_on(dev, stream))
     if rc != 0:
         raise KdaError("kda_pool_clear", rc)
 
@@ -879,7 +896,7 @@ def kda_pool_compact(pools, slots, done=None, *, out=None, workspace=None, strea
     if done is not None:
         _check(done, "done", (B,), torch.uint8 if done.dtype == torch.uint8 else torch.bool, dev)
     if out is None:
-        out = _empty((B,), torch.int32, dev, stream)
+        out = _empty((B,), torch.int32, dev, stream, slots)
     else:
         _check(out, "out", (B,), torch.int32, dev)
     if workspace is None:
@@ -888,7 +905,7 @@ def kda_pool_compact(pools, slots, done=None, *, out=None, workspace=None, strea
         _check(workspace, "workspace", (n_slots + 1,), torch.int32, dev)
     with _on_device(dev):
         rc = lib().kda_pool_compact(to, len(pools), n_slots, slots.data_ptr(), _ptr(done), out.data_ptr(), B,
-                                    workspace.data_ptr(), _stream_handle(stream))
+                                    workspace.data_ptr(), _stream_on(dev, stream))
     if rc != 0:
         raise KdaError("kda_pool_compact", rc)
     return out
