@@ -30,7 +30,8 @@
 // columns) for that.  The weighted x is transposed on its way by ldmatrix and the 16x128b stores, whose
 // fragments have one layout.
 //
-// Warps (18): 0-3 state, 4-7 decays and weighted x, 8-15 Q and outputs, 16 products, 17 loads.
+// Warps (20): 0-3 state, 4-7 decays and weighted x, 8-15 Q and outputs, 16 products, 17 loads of B and x,
+// 18 loads of C, 19 stores of y.
 // Tensor memory (512 columns): S^T, Y, G (then Q in its place), weighted x hi and lo.
 // Order of the products: Y = C S | S += hi | Y += Q X | S += lo | next G.  The scaling of Y runs under
 // the hi part, Y's store under the lo part, the state's conversion under the next G.
@@ -56,10 +57,11 @@ using namespace sm100;
 constexpr int kTok = 128;                    // tokens per chunk
 constexpr int kCols = 128;                   // value columns per CTA
 constexpr int kStages = 2;
-constexpr int kThreads = 576;
+constexpr int kThreads = 640;
 constexpr int kStateWarps = 4, kDecayWarps = 4, kScoreWarps = 8;
 constexpr int kFirstDecay = kStateWarps, kFirstScore = kFirstDecay + kDecayWarps;
-constexpr int kIssueWarp = kFirstScore + kScoreWarps, kLoadWarp = kIssueWarp + 1;
+constexpr int kIssueWarp = kFirstScore + kScoreWarps, kLoadWarp = kIssueWarp + 1,
+              kLoadCWarp = kLoadWarp + 1, kStoreWarp = kLoadCWarp + 1;
 constexpr uint32_t ATOM = 16384;             // [128 rows][64 columns] bf16, 128-byte swizzle
 constexpr uint32_t kTile = 2 * ATOM;
 
@@ -286,7 +288,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     const uint32_t sb = smem_u32(sm);
     __shared__ Scalars scal[2];
     __shared__ uint64_t full[kStages], empty[kStages], full_c, bar_scal[2], bar_g, bar_cs, bar_upd, bar_px, bar_state, bar_w, bar_q,
-        bar_yfree, bar_staged, bar_drain;
+        bar_yfree, bar_staged, yread[kStages], bar_drain;
     __shared__ uint32_t tmem_base_s;
     __shared__ volatile int abort_s;
     __shared__ int seq_s, seg_s;
@@ -359,7 +361,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     const int row0 = (p.cu_seqlens ? (int)start : 0) + tok0;             // token coordinate of the first chunk
 
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); mbar_init(&yread[i], 1); }
         for (int i = 0; i < 2; ++i) mbar_init(&bar_scal[i], kDecayWarps);
         mbar_init(&full_c, 1);
         mbar_init(&bar_g, 1);
@@ -390,58 +392,62 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     const int quarter = warp & 3;
 
     if (warp == kLoadWarp) {
-        // ------------------------------------------------------------ loads, and the stores of y
+        // ------------------------------------------------------------ loads of B and x
         if (lane == 0) {
-            constexpr int na = N / 64;
-            int issued = 0, issued_c = 0;
-            auto load_bx = [&](int c) {
+            int issued = 0;
+            for (int c = 0; c < chunks; ++c) {
                 const int st = c % kStages, t = row0 + c * kTok;
                 uint8_t* s = sm + st * kStageBytes;
-                mbar_arrive_expect_tx(&full[st], ATOM * (2 + na));
-                for (int i = 0; i < na; ++i) tma_load_4d(s + OFF_B + i * ATOM, &tm_b, &full[st], 64 * i, g, t, row_seq);
+                // the stage is free after the last product of two chunks ago and once its y has been read out
+                if (c >= kStages && (!wait.one(&empty[st], (uint32_t)(c / kStages - 1) & 1) ||
+                                     (!STATE_ONLY && !wait.one(&yread[st], (uint32_t)(c / kStages - 1) & 1))))
+                    break;
+                mbar_arrive_expect_tx(&full[st], ATOM * (2 + N / 64));
+                for (int i = 0; i < N / 64; ++i) tma_load_4d(s + OFF_B + i * ATOM, &tm_b, &full[st], 64 * i, g, t, row_seq);
                 for (int i = 0; i < 2; ++i)
                     tma_load_4d(s + OFF_X + i * ATOM, &tm_x, &full[st], NH == 2 ? 0 : 64 * i, NH == 2 && i ? h1 : h0, t, row_seq);
                 ++issued;
-            };
-            auto load_c = [&](int c) {
-                mbar_arrive_expect_tx(&full_c, ATOM * na);
-                for (int i = 0; i < na; ++i)
-                    tma_load_4d(sm + OFF_C + i * ATOM, &tm_c, &full_c, 64 * i, g, row0 + c * kTok, row_seq);
-                ++issued_c;
-            };
-            if (chunks > 0) load_bx(0);
-            if (chunks > 0 && !STATE_ONLY) load_c(0);
-            if (chunks > 1) load_bx(1);
-            for (int c = 0; c < chunks; ++c) {
-                const int st = c % kStages;
-                if (!STATE_ONLY) {
-                    if (c + 1 < chunks) {
-                        if (!wait.one(&bar_cs, c & 1)) break;            // the chunk's C is used up
-                        load_c(c + 1);
-                    }
-                    // y of the chunk, staged in its x tile: whole tiles, clipped at the end of the tensor
-                    if (!wait.one(&bar_staged, c & 1)) break;
-                    if (!p.cu_seqlens || len - c * kTok >= kTok) {
-                        for (int i = 0; i < 2; ++i)
-                            if (!(NH == 2 && i == 1 && h1 == h0))
-                                tma_store_4d(&tm_y, sm + st * kStageBytes + OFF_X + i * ATOM, NH == 2 ? 0 : 64 * i,
-                                             NH == 2 && i ? h1 : h0, row0 + c * kTok, row_seq);
-                        bulk_commit_group();
-                        bulk_wait_read_all();
-                    }
-                }
-                if (c + kStages < chunks) {
-                    if (!wait.one(&empty[st], (uint32_t)(c / kStages) & 1)) break;
-                    load_bx(c + kStages);
-                }
+                // x of the stage's next turn, which no other CTA reads, into L2 (3% at P = 128)
+                if (c + kStages < chunks)
+                    for (int i = 0; i < 2; ++i)
+                        tma_prefetch_4d(&tm_x, NH == 2 ? 0 : 64 * i, NH == 2 && i ? h1 : h0, t + kStages * kTok, row_seq);
             }
             // nothing may be in flight when the CTA exits
-            bulk_wait_all();
             for (int c = max(0, issued - kStages); c < issued; ++c)
                 if (!mbar_wait(&full[c % kStages], (uint32_t)(c / kStages) & 1, p.timeout_ns))
                     report_status(p.status, KDA_ERR_TIMEOUT);
-            if (issued_c > 0 && !mbar_wait(&full_c, (uint32_t)(issued_c - 1) & 1, p.timeout_ns))
+        }
+    } else if (warp == kLoadCWarp) {
+        // ------------------------------------------------------------ loads of C, each as soon as the last is used up
+        if (lane == 0 && !STATE_ONLY) {
+            int issued = 0;
+            for (int c = 0; c < chunks; ++c) {
+                if (c > 0 && !wait.one(&bar_cs, (uint32_t)(c - 1) & 1)) break;
+                mbar_arrive_expect_tx(&full_c, kTile / 128 * N);
+                for (int i = 0; i < N / 64; ++i)
+                    tma_load_4d(sm + OFF_C + i * ATOM, &tm_c, &full_c, 64 * i, g, row0 + c * kTok, row_seq);
+                ++issued;
+            }
+            if (issued > 0 && !mbar_wait(&full_c, (uint32_t)(issued - 1) & 1, p.timeout_ns))
                 report_status(p.status, KDA_ERR_TIMEOUT);
+        }
+    } else if (warp == kStoreWarp) {
+        // ------------------------------------------------------------ stores of y from the x tiles
+        if (lane == 0 && !STATE_ONLY) {
+            for (int c = 0; c < chunks; ++c) {
+                const int st = c % kStages;
+                if (!wait.one(&bar_staged, c & 1)) break;
+                if (!p.cu_seqlens || len - c * kTok >= kTok) {           // whole tiles, clipped at the end of the tensor
+                    for (int i = 0; i < 2; ++i)
+                        if (!(NH == 2 && i == 1 && h1 == h0))
+                            tma_store_4d(&tm_y, sm + st * kStageBytes + OFF_X + i * ATOM, NH == 2 ? 0 : 64 * i,
+                                         NH == 2 && i ? h1 : h0, row0 + c * kTok, row_seq);
+                    bulk_commit_group();
+                    bulk_wait_read_all();
+                }
+                mbar_arrive(&yread[st]);
+            }
+            bulk_wait_all();
         }
     } else if (warp == kIssueWarp) {
         // ------------------------------------------------------------ products
@@ -714,7 +720,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 ok = named_bar_and(3 + quarter, 64, ok);
                 if (!ok) break;
                 tc_fence_after_sync();
-#pragma unroll 1
+#pragma unroll
                 for (int i = 0; i < NH; ++i) {
                     const uint32_t qt = tbase + TM_G + 64 * i + lanes + 8 * which;
                     const float* colf = sc.col[i] + 16 * which;
