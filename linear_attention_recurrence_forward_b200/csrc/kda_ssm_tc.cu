@@ -36,10 +36,11 @@
 // Order of the products: Y = C S | S += hi | Y += Q X | S += lo | next G.  The scaling of Y runs under
 // the hi part, Y's store under the lo part, the state's conversion under the next G.
 //
-// Long prompts with few heads: the tokens are cut into segments.  A first launch runs the state update
-// alone (B and x only) on every segment but the last, the first one from S0, the others from zero; the
-// second starts each segment from the segments before it, S <- 2^{total} S + local, folded in as it loads
-// its start state.
+// Long prompts with few heads: the tokens are cut into segments.  A first launch forms the state of every
+// segment but the last (B and x only; the first one from S0, the others from zero), going through the
+// chunks backwards, so that the weights hold the decay to the segment's end and the products just add up;
+// the second starts each segment from the segments before it, S <- 2^{total} S + local, folded in as it
+// loads its start state.
 //
 // Every wait is bounded in time; a wait that runs out sets the status word and an abort flag that ends
 // the other warps' waits, the products and loads in flight are drained, and the CTA returns.
@@ -56,7 +57,7 @@ using namespace sm100;
 
 constexpr int kTok = 128;                    // tokens per chunk
 constexpr int kCols = 128;                   // value columns per CTA
-constexpr int kStages = 2;
+constexpr int kStages = 2;                   // of B and x; the state-only kernel has three (no C, no S)
 constexpr int kThreads = 640;
 constexpr int kStateWarps = 4, kDecayWarps = 4, kScoreWarps = 8;
 constexpr int kFirstDecay = kStateWarps, kFirstScore = kFirstDecay + kDecayWarps;
@@ -71,7 +72,7 @@ constexpr uint32_t OFF_B = 0, OFF_X = kTile, kStageBytes = 2 * kTile;
 constexpr uint32_t OFF_C = kStages * kStageBytes, OFF_S = OFF_C + kTile;
 constexpr uint32_t SMEM_DYN = OFF_S + kTile + 1024;
 
-// tensor memory columns
+// tensor memory columns (the state-only kernel's three groups have their weighted x at TM_HI, TM_G and TM_Y)
 constexpr uint32_t TM_S = 0, TM_Y = 128, TM_G = 256, TM_HI = 384, TM_LO = 448, TM_COLS = 512;
 
 struct __align__(16) Scalars {               // of one chunk, per head of the tile
@@ -209,6 +210,18 @@ __device__ __forceinline__ void tmem_read64(uint32_t taddr, float* r) {
         : "r"(taddr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_read32(uint32_t taddr, float* r) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&r"(u[0]), "=&r"(u[1]), "=&r"(u[2]), "=&r"(u[3]), "=&r"(u[4]), "=&r"(u[5]), "=&r"(u[6]), "=&r"(u[7]),
+          "=&r"(u[8]), "=&r"(u[9]), "=&r"(u[10]), "=&r"(u[11]), "=&r"(u[12]), "=&r"(u[13]), "=&r"(u[14]), "=&r"(u[15]),
+          "=&r"(u[16]), "=&r"(u[17]), "=&r"(u[18]), "=&r"(u[19]), "=&r"(u[20]), "=&r"(u[21]), "=&r"(u[22]), "=&r"(u[23]),
+          "=&r"(u[24]), "=&r"(u[25]), "=&r"(u[26]), "=&r"(u[27]), "=&r"(u[28]), "=&r"(u[29]), "=&r"(u[30]), "=&r"(u[31])
+        : "r"(taddr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_write32(uint32_t taddr, const float* r) {
     const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
     asm volatile(
@@ -282,16 +295,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
                   const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_y, const Params p) {
     constexpr int NH = P == 64 ? 2 : 1;      // heads per tile
+    constexpr int ST = STATE_ONLY ? 3 : kStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_u32(smem_raw);
     uint8_t* sm = smem_raw + (((raw_base + 1023u) & ~1023u) - raw_base);
     const uint32_t sb = smem_u32(sm);
-    __shared__ Scalars scal[2];
-    __shared__ uint64_t full[kStages], empty[kStages], full_c, bar_scal[2], bar_g, bar_cs, bar_upd, bar_px, bar_state, bar_w, bar_q,
+    __shared__ Scalars scal[STATE_ONLY ? 3 : 2];
+    __shared__ uint64_t full[ST], empty[ST], full_c, bar_scal[2], bar_g, bar_cs, bar_upd[3], bar_px, bar_state, bar_w, bar_wst[3],
+        bar_behind[3], bar_init, bar_q,
         bar_yfree, bar_staged, yread[kStages], bar_drain;
     __shared__ uint32_t tmem_base_s;
     __shared__ volatile int abort_s;
     __shared__ int seq_s, seg_s;
+    __shared__ float seg_total_s[2], behind_s[3][2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int H = p.H;
 
@@ -361,17 +377,21 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     const int row0 = (p.cu_seqlens ? (int)start : 0) + tok0;             // token coordinate of the first chunk
 
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); mbar_init(&yread[i], 1); }
+        for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < kStages; ++i) mbar_init(&yread[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&bar_scal[i], kDecayWarps);
         mbar_init(&full_c, 1);
         mbar_init(&bar_g, 1);
+        mbar_init(&bar_init, N / 8);
         mbar_init(&bar_cs, 1);
-        mbar_init(&bar_upd, 1);
+        for (int i = 0; i < 3; ++i) mbar_init(&bar_upd[i], 1);
         mbar_init(&bar_px, 1);
+        static_assert(kStateWarps == kDecayWarps, "bar_state counts either");
         mbar_init(&bar_state, kStateWarps);
         mbar_init(&bar_yfree, kScoreWarps);
         mbar_init(&bar_staged, kScoreWarps);
         mbar_init(&bar_w, kDecayWarps);
+        for (int i = 0; i < 3; ++i) { mbar_init(&bar_wst[i], kDecayWarps); mbar_init(&bar_behind[i], kDecayWarps); }
         mbar_init(&bar_q, kScoreWarps);
         mbar_init(&bar_drain, 1);
         fence_mbar_init();
@@ -391,16 +411,63 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;            // this warp's tensor-memory lanes
     const int quarter = warp & 3;
 
+    // ---- states: a lane of a warp is one value column, in the warp's quarter of the tensor-memory lanes
+    const int col = 32 * quarter + lane;                                // value column of this lane
+    const int half = NH == 2 ? col >> 6 : 0;
+    const int head = half ? h1 : h0, pc = NH == 2 ? col & 63 : col;
+    const bool dup = NH == 2 && half == 1 && h1 == h0;               // carried, not stored
+    const size_t s_off = (((size_t)seq * H + head) * N) * P + pc;    // S[seq][head][0][pc]
+    auto seg_state = [&](int u) { return p.seg_state + ((size_t)u * H + head) * N * P + pc; };
+    auto store_state = [&](float* to, int n0, const float* v) {
+        if (!dup) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) to[(size_t)(n0 + i) * P] = v[i];
+        }
+    };
+    // The start state of 32 rows n.  Sequences of several segments: the first launch starts segment 0 from
+    // S0, and leaves a copy of S0 in the last segment's place, which no local state takes; the second launch
+    // reads S0 nowhere else, so that S_T may be S0.
+    auto load_start = [&](int n0, float* v) {
+        const float* from = STATE_ONLY || n_seg == 1 ? (p.S0 && seg == 0 ? p.S0 + s_off : nullptr)
+                                                     : seg_state(seg == 0 ? unit0 + n_seg - 1 : unit0);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = from ? from[(size_t)(n0 + i) * P] : 0.f;
+        if constexpr (STATE_ONLY) {
+            if (seg == 0) store_state(seg_state(unit0 + n_seg - 1), n0, v);
+        } else {
+#pragma unroll 2
+            for (int k = 1; k < seg; ++k) {
+                const float d = ex2(p.seg_decay[(size_t)(unit0 + k) * H + head]);
+                const float* l = seg_state(unit0 + k);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = fmaf(d, v[i], l[(size_t)(n0 + i) * P]);
+            }
+        }
+    };
+    // 32 rows to each group of four warps, in parallel (each start state is as many dependent reads as segments)
+    if (!STATE_ONLY && warp < kIssueWarp && 8 * (warp & ~3) < N) {
+        const int n0 = 8 * (warp & ~3);
+        float v[32];
+        load_start(n0, v);
+        if (chunks > 0) {
+            tmem_write32(tbase + TM_S + lanes + n0, v);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            warp_arrive(&bar_init, lane);
+        } else if (p.ST) {
+            store_state(p.ST + s_off, n0, v);            // an empty sequence
+        }
+    }
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads of B and x
         if (lane == 0) {
             int issued = 0;
             for (int c = 0; c < chunks; ++c) {
-                const int st = c % kStages, t = row0 + c * kTok;
+                const int st = c % ST, t = row0 + (STATE_ONLY ? chunks - 1 - c : c) * kTok;
                 uint8_t* s = sm + st * kStageBytes;
-                // the stage is free after the last product of two chunks ago and once its y has been read out
-                if (c >= kStages && (!wait.one(&empty[st], (uint32_t)(c / kStages - 1) & 1) ||
-                                     (!STATE_ONLY && !wait.one(&yread[st], (uint32_t)(c / kStages - 1) & 1))))
+                // the stage is free after the last product of its last turn and once its y has been read out
+                if (c >= ST && (!wait.one(&empty[st], (uint32_t)(c / ST - 1) & 1) ||
+                                (!STATE_ONLY && !wait.one(&yread[st % kStages], (uint32_t)(c / ST - 1) & 1))))
                     break;
                 mbar_arrive_expect_tx(&full[st], ATOM * (2 + N / 64));
                 for (int i = 0; i < N / 64; ++i) tma_load_4d(s + OFF_B + i * ATOM, &tm_b, &full[st], 64 * i, g, t, row_seq);
@@ -408,13 +475,14 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     tma_load_4d(s + OFF_X + i * ATOM, &tm_x, &full[st], NH == 2 ? 0 : 64 * i, NH == 2 && i ? h1 : h0, t, row_seq);
                 ++issued;
                 // x of the stage's next turn, which no other CTA reads, into L2 (3% at P = 128)
-                if (c + kStages < chunks)
+                if (c + ST < chunks)
                     for (int i = 0; i < 2; ++i)
-                        tma_prefetch_4d(&tm_x, NH == 2 ? 0 : 64 * i, NH == 2 && i ? h1 : h0, t + kStages * kTok, row_seq);
+                        tma_prefetch_4d(&tm_x, NH == 2 ? 0 : 64 * i, NH == 2 && i ? h1 : h0,
+                                        STATE_ONLY ? t - ST * kTok : t + ST * kTok, row_seq);
             }
             // nothing may be in flight when the CTA exits
-            for (int c = max(0, issued - kStages); c < issued; ++c)
-                if (!mbar_wait(&full[c % kStages], (uint32_t)(c / kStages) & 1, p.timeout_ns))
+            for (int c = max(0, issued - ST); c < issued; ++c)
+                if (!mbar_wait(&full[c % ST], (uint32_t)(c / ST) & 1, p.timeout_ns))
                     report_status(p.status, KDA_ERR_TIMEOUT);
         }
     } else if (warp == kLoadCWarp) {
@@ -464,6 +532,18 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 return true;
             };
             bool ok = STATE_ONLY || chunks == 0 || issue_g(0);
+            if constexpr (STATE_ONLY) {
+                for (int c = 0; c < chunks; ++c) {
+                    const uint32_t s = sb + (c % ST) * kStageBytes, w = tbase + TM_HI - 128 * (c % ST);
+                    if (!wait.one(&bar_wst[c % ST], (uint32_t)(c / ST) & 1)) break;
+                    tc_fence_after_sync();
+                    issue_ts(tbase + TM_S, w, s + OFF_B, id_up, c > 0);
+                    issue_ts(tbase + TM_S, w + 64, s + OFF_B, id_up, true);
+                    mma_commit(&bar_upd[c % ST]);
+                    mma_commit(&empty[c % ST]);
+                }
+                ok = false;
+            }
             for (int c = 0; c < chunks && ok; ++c) {
                 const uint32_t s = sb + (c % kStages) * kStageBytes, par = c & 1;
                 ok = wait.one(&bar_state, par);          // S as bf16 and decayed
@@ -488,7 +568,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     mma_commit(&bar_px);
                 }
                 issue_ts(tbase + TM_S, tbase + TM_LO, s + OFF_B, id_up, true);
-                mma_commit(&bar_upd);
+                mma_commit(&bar_upd[0]);
                 mma_commit(&empty[c % kStages]);
                 if (!STATE_ONLY && c + 1 < chunks) ok = issue_g(c + 1);
             }
@@ -497,50 +577,12 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         }
     } else if (warp < kStateWarps) {
         // ------------------------------------------------------------ state
-        const int col = 32 * warp + lane;                                // value column of this lane
-        const int half = NH == 2 ? col >> 6 : 0;
-        const int head = half ? h1 : h0, pc = NH == 2 ? col & 63 : col;
-        const bool dup = NH == 2 && half == 1 && h1 == h0;               // carried, not stored
-        const size_t s_off = (((size_t)seq * H + head) * N) * P + pc;    // S[seq][head][0][pc]
-        auto seg_state = [&](int u) { return p.seg_state + ((size_t)u * H + head) * N * P + pc; };
-        auto store_state = [&](float* to, int n0, const float* v) {
-            if (!dup) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) to[(size_t)(n0 + i) * P] = v[i];
-            }
-        };
-        // The start state of 32 rows n.  Sequences of several segments: the first launch starts segment 0 from
-        // S0, and leaves a copy of S0 in the last segment's place, which no local state takes; the second launch
-        // reads S0 nowhere else, so that S_T may be S0.
-        auto load_start = [&](int n0, float* v) {
-            const float* from = STATE_ONLY || n_seg == 1 ? (p.S0 && seg == 0 ? p.S0 + s_off : nullptr)
-                                                         : seg_state(seg == 0 ? unit0 + n_seg - 1 : unit0);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = from ? from[(size_t)(n0 + i) * P] : 0.f;
-            if constexpr (STATE_ONLY) {
-                if (seg == 0) store_state(seg_state(unit0 + n_seg - 1), n0, v);
-            } else {
-#pragma unroll 2
-                for (int k = 1; k < seg; ++k) {
-                    const float d = ex2(p.seg_decay[(size_t)(unit0 + k) * H + head]);
-                    const float* l = seg_state(unit0 + k);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = fmaf(d, v[i], l[(size_t)(n0 + i) * P]);
-                }
-            }
-        };
-        for (int n0 = 0; n0 < N; n0 += 32) {
-            float v[32];
-            load_start(n0, v);
-            if (chunks > 0) tmem_write32(tbase + TM_S + lanes + n0, v);
-            else if (p.ST) store_state(p.ST + s_off, n0, v);             // an empty sequence
-        }
-        tmem_wait_st();
         bool ok = true;
-        for (int c = 0; c < chunks && ok; ++c) {
+        for (int c = 0; !STATE_ONLY && c < chunks && ok; ++c) {
             const uint32_t par = c & 1;
             const Scalars& sc = scal[c & 1];
-            ok = wait.warp(&bar_scal[c & 1], (c >> 1) & 1) && (c == 0 || wait.warp(&bar_upd, par ^ 1));
+            ok = wait.warp(&bar_scal[c & 1], (c >> 1) & 1) &&
+                 (c == 0 ? wait.warp(&bar_init, 0) : wait.warp(&bar_upd[0], par ^ 1));
             if (!ok) break;
             tc_fence_after_sync();
             const float decay = ex2((sc.total[half][0] + sc.total[half][1]) + (sc.total[half][2] + sc.total[half][3]));
@@ -550,13 +592,11 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 float v[64];
                 const uint32_t ta = tbase + TM_S + lanes + n0;
                 tmem_read64(ta, v);
-                if (!STATE_ONLY) {
 #pragma unroll
-                    for (int i = 0; i < 64; i += 8)
-                        *reinterpret_cast<uint4*>(sm + OFF_S + sw128_offset(col, n0 + i, ATOM)) =
-                            make_uint4(bf16x2(v[i], v[i + 1]), bf16x2(v[i + 2], v[i + 3]), bf16x2(v[i + 4], v[i + 5]),
-                                       bf16x2(v[i + 6], v[i + 7]));
-                }
+                for (int i = 0; i < 64; i += 8)
+                    *reinterpret_cast<uint4*>(sm + OFF_S + sw128_offset(col, n0 + i, ATOM)) =
+                        make_uint4(bf16x2(v[i], v[i + 1]), bf16x2(v[i + 2], v[i + 3]), bf16x2(v[i + 4], v[i + 5]),
+                                   bf16x2(v[i + 6], v[i + 7]));
                 scale_by<64>(v, decay);
                 tmem_write32(ta, v);
                 tmem_write32(ta + 32, v + 32);
@@ -566,21 +606,35 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             tc_fence_before_sync();
             if (!(p.skip_handoff && c == 0)) warp_arrive(&bar_state, lane);
         }
-        // the state after the last token (of the sequence; of the segment in the first launch)
-        if (ok && chunks > 0 && (STATE_ONLY || (last_seg && p.ST)) && wait.warp(&bar_upd, (chunks - 1) & 1)) {
+        if constexpr (STATE_ONLY) {
+            // the segment's state: the sum of its chunks, and for the first segment what is left of S0
+            ok = wait.warp(&bar_state, 0) && wait.warp(&bar_upd[(chunks - 1) % ST], (uint32_t)((chunks - 1) / ST) & 1);
+            tc_fence_after_sync();
+            const float decay = ex2(seg_total_s[half]);
+#pragma unroll 1
+            for (int n0 = 0; n0 < N && ok; n0 += 32) {
+                float v[32], start[32];
+                tmem_read32(tbase + TM_S + lanes + n0, v);
+                load_start(n0, start);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = fmaf(decay, start[i], v[i]);
+                store_state(seg_state(unit), n0, v);
+            }
+        } else if (ok && chunks > 0 && last_seg && p.ST && wait.warp(&bar_upd[0], (chunks - 1) & 1)) {
+            // the state after the last token
             tc_fence_after_sync();
 #pragma unroll 1
-            for (int n0 = 0; n0 < N; n0 += 64) {
-                float v[64];
-                tmem_read64(tbase + TM_S + lanes + n0, v);
-                float* to = STATE_ONLY ? seg_state(unit) : p.ST + s_off;
-                store_state(to, n0, v);
-                store_state(to, n0 + 32, v + 32);
+            for (int n0 = 0; n0 < N; n0 += 32) {
+                float v[32];
+                tmem_read32(tbase + TM_S + lanes + n0, v);
+                store_state(p.ST + s_off, n0, v);
             }
         }
-    } else if (warp < kFirstScore) {
+    } else if (warp < (STATE_ONLY ? kIssueWarp : kFirstScore)) {
         // ------------------------------------------------------------ decays and weighted x
-        const int dw = warp - kFirstDecay;
+        // one group of four warps; in the state-only kernel three, each every third chunk
+        const int dw = (warp - kFirstDecay) & 3, group = (warp - kFirstDecay) >> 2;
+        constexpr int kGroups = STATE_ONLY ? ST : 1;
         const int j = 32 * dw + lane;                                    // a token here
         float rate[NH], bias[NH], raw[NH], total_all[NH];
 #pragma unroll
@@ -590,17 +644,20 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             bias[i] = p.dt_bias ? p.dt_bias[head] : 0.f;
             total_all[i] = 0.f;
         }
+        // the state-only kernel goes through its chunks from the last to the first: the decay behind a chunk is then
+        // known when its weights are formed, and the products only add up, with no pass over the state in between
+        auto chunk_at = [&](int c) { return STATE_ONLY ? chunks - 1 - c : c; };
         auto load_dt = [&](int c) {
-            const int t = c * kTok + j;
+            const int t = chunk_at(c) * kTok + j;
 #pragma unroll
             for (int i = 0; i < NH; ++i)
                 raw[i] = t < len ? load_elem(p.dt, (start + tok0 + t) * p.lddt + (i ? h1 : h0)) : 0.f;
         };
-        load_dt(0);
+        load_dt(group);
         bool ok = true;
-        for (int c = 0; c < chunks; ++c) {
-            Scalars& sc = scal[c & 1];
-            const int n_valid = min(kTok, len - c * kTok);
+        for (int c = group; c < chunks; c += kGroups) {
+            Scalars& sc = scal[STATE_ONLY ? group : c & 1];
+            const int n_valid = min(kTok, len - chunk_at(c) * kTok);
             float sfx[NH], stp[NH];
 #pragma unroll
             for (int i = 0; i < NH; ++i) stp[i] = raw[i] + bias[i];
@@ -628,8 +685,14 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 sc.col[i][j] = stp[i] * ex2(sfx[i]);
                 if (lane == 31) sc.total[i][dw] = incl;
             }
-            if (c + 1 < chunks) load_dt(c + 1);
-            named_bar_sync(1, 32 * kDecayWarps);
+            if (c + kGroups < chunks) load_dt(c + kGroups);
+            named_bar_sync(1 + 2 * group, 32 * kDecayWarps);
+            if constexpr (STATE_ONLY) {
+                // the decay behind the chunk, handed on from group to group
+                if (c > 0) (void)wait.warp(&bar_behind[group], (uint32_t)((c - 1) / ST) & 1);
+#pragma unroll
+                for (int i = 0; i < NH; ++i) total_all[i] = c > 0 ? behind_s[group][i] : 0.f;
+            }
 #pragma unroll
             for (int i = 0; i < NH; ++i) {
                 float after = 0.f, all = 0.f;
@@ -638,15 +701,22 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     if (b > dw) after += sc.total[i][b];
                     all += sc.total[i][b];
                 }
-                const float w = stp[i] * ex2(sfx[i] + after);
+                const float w = stp[i] * ex2(sfx[i] + after + (STATE_ONLY ? total_all[i] : 0.f));
                 const __nv_bfloat16 w1 = __float2bfloat16_rn(w), w2 = __float2bfloat16_rn(w - __bfloat162float(w1));
                 sc.w1[i][j] = __bfloat16_as_ushort(w1);
                 sc.w2[i][j] = __bfloat16_as_ushort(w2);
                 total_all[i] += all;
             }
-            warp_arrive(&bar_scal[c & 1], lane);
-            ok = wait.warp(&full[c % kStages], (uint32_t)(c / kStages) & 1);
-            uint8_t* s = sm + (c % kStages) * kStageBytes;
+            if constexpr (STATE_ONLY) {
+                const int next = (group + 1) % ST;
+                if (j == 0)
+                    for (int i = 0; i < NH; ++i) behind_s[next][i] = total_all[i];
+                warp_arrive(&bar_behind[next], lane);
+            } else {
+                warp_arrive(&bar_scal[c & 1], lane);
+            }
+            ok = wait.warp(&full[c % ST], (uint32_t)(c / ST) & 1);
+            uint8_t* s = sm + (c % ST) * kStageBytes;
             if (ok && p.cu_seqlens && j >= n_valid) {
                 // rows of other sequences, or of none: zeros, so that nothing of theirs enters a sum
                 const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -656,9 +726,11 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 }
                 fence_proxy_async_smem();
             }
-            if (ok && c > 0) ok = wait.warp(&bar_upd, (uint32_t)(c - 1) & 1);   // the operand's space is free
+            // the operand's place is free
+            if constexpr (STATE_ONLY) ok = ok && (c < ST || wait.warp(&bar_upd[group], (uint32_t)(c / ST - 1) & 1));
+            else ok = ok && (c == 0 || wait.warp(&bar_upd[0], (uint32_t)(c - 1) & 1));
             // w and the zeros of all tokens; all four warps leave together
-            ok = named_bar_and(2, 32 * kDecayWarps, ok);
+            ok = named_bar_and(2 + 2 * group, 32 * kDecayWarps, ok);
             if (!ok) break;
             tc_fence_after_sync();
             // 32 value columns per warp, 32 tokens a step
@@ -686,18 +758,22 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const uint32_t at = tbase + lanes + ((uint32_t)(16 * u) << 16) + 16 * q4;
-                    tmem_st_16x128(at + TM_HI, hi[u]);
-                    tmem_st_16x128(at + TM_LO, lo[u]);
+                    const uint32_t at = tbase + lanes + ((uint32_t)(16 * u) << 16) + 16 * q4 + TM_HI - 128 * group;
+                    tmem_st_16x128(at, hi[u]);
+                    tmem_st_16x128(at + 64, lo[u]);
                 }
             }
             tmem_wait_st();
             tc_fence_before_sync();
-            warp_arrive(&bar_w, lane);
+            warp_arrive(STATE_ONLY ? &bar_wst[group] : &bar_w, lane);
         }
-        if (STATE_ONLY && ok && j == 0) {
-            p.seg_decay[(size_t)unit * H + h0] = total_all[0];
-            if (NH == 2 && h1 != h0) p.seg_decay[(size_t)unit * H + h1] = total_all[NH - 1];
+        if constexpr (STATE_ONLY) if (group == (chunks - 1) % ST) {
+            if (ok && j == 0) {
+                p.seg_decay[(size_t)unit * H + h0] = seg_total_s[0] = total_all[0];
+                if (NH == 2 && h1 != h0) p.seg_decay[(size_t)unit * H + h1] = total_all[NH - 1];
+                seg_total_s[1] = total_all[NH - 1];
+            }
+            warp_arrive(&bar_state, lane);
         }
     } else if (!STATE_ONLY) {
         // ------------------------------------------------------------ Q (the decayed lower triangle of G), outputs
@@ -837,7 +913,7 @@ int tiles_of(int H, int G, int P) {
 // through the state-only launch and all of them, k times as many CTAs, through the second.  The least of the modelled
 // times is taken, in waves of 148 CTAs and units of a chunk of the full kernel: a state-only chunk costs kStateCost of
 // one, the second launch and the start states about kSplitCost chunks.
-constexpr double kStateCost = 0.55, kSplitCost = 4.0;
+constexpr double kStateCost = 0.27, kSplitCost = 6.0;
 constexpr int kMostSegments = 8;
 
 int segment_chunks(int n_seq, long long T_total, int H, int P) {
