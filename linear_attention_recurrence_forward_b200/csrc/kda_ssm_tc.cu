@@ -20,21 +20,25 @@
 // each term of y.  The state itself is fp32: B and x are exact bf16 operands, and a weight w = w1 + w2
 // (two bf16 values, off by at most 2^-16 w) makes the weighted x the sum of two bf16 values,
 // hi = x w1 rounded and lo = x w2 + (x w1 - hi) rounded (x w1 - hi is exact), so a term of the state is
-// off by at most 3 * 2^-16 of itself.  One bf16 value would leave 2^-8, a third product costs a fifth
-// more tensor time.
+// off by at most 3 * 2^-16 of itself.
 //
-// What bounds it: HBM moves 64 KB of x and y per chunk of a 128-column tile (2.8K cycles at the
-// measured copy rate), the tensor core needs 2.5K cycles, and its operands with the tiles' own traffic
-// about 3.5K cycles of shared memory, so operands are kept out of shared memory where a product allows:
-// Q and the weighted x are tensor-memory operands, and the state is held transposed (lanes = value
-// columns) for that.  The weighted x is transposed on its way by ldmatrix and the 16x128b stores, whose
-// fragments have one layout.
+// What bounds it.  Per chunk of a 128-column tile HBM moves 64 KB of x and y (2.8K cycles at the measured
+// copy rate with all SMs at it), the tensor core needs 2.5K cycles, and shared memory 3.5K (the products'
+// operands and the tiles' own way in and out).  A chunk takes about 5.5K (4 x 8192 tokens, 96 heads of 128:
+// 590 us, 3.0 TB/s of x and y), and the arithmetic warps are at work in nearly all of them: their chain of steps,
+// each a pass from tensor memory through registers and back, is what bounds it.  So operands are kept out of
+// shared memory where a product allows: Q and the weighted x are tensor-memory operands, and the state is
+// held transposed (lanes = value columns) for that.  The weighted x is transposed on its way by ldmatrix and
+// the 16x128b stores, whose fragments have one layout.
 //
-// Warps (20): 0-3 state, 4-7 decays and weighted x, 8-15 Q and outputs, 16 products, 17 loads of B and x,
-// 18 loads of C, 19 stores of y.
-// Tensor memory (512 columns): S^T, Y, G (then Q in its place), weighted x hi and lo.
-// Order of the products: Y = C S | S += hi | Y += Q X | S += lo | next G.  The scaling of Y runs under
-// the hi part, Y's store under the lo part, the state's conversion under the next G.
+// Sixteen warps do every step together, a quarter of the columns or tokens to a group of four, in an order
+// that lets the products run behind them: Q while Y = C S runs, the next chunk's weighted x and
+// carried state while Q X runs.  Four more warps issue the products, move the tiles, and form the decays two
+// chunks ahead; the products and the copies follow one another in one thread each.  Warps that keep
+// to one step each, 21 of them, took 10 % longer with two heads to a tile (480 against 424 us at 4 x 8192
+// tokens, 96 heads of 64; 894 against 788 us at 65536) and the same with one.  x has three stages: a tile is y's place when it is done,
+// and is read out (1.8K cycles) while the next two are at work; B and C have one, free once the state is
+// updated.  Tensor memory (512 columns): S^T, Y, G (then Q in its place), weighted x hi and lo.
 //
 // Long prompts with few heads: the tokens are cut into segments.  A first launch forms the state of every
 // segment but the last (B and x only; the first one from S0, the others from zero), going through the
@@ -57,23 +61,23 @@ using namespace sm100;
 
 constexpr int kTok = 128;                    // tokens per chunk
 constexpr int kCols = 128;                   // value columns per CTA
-constexpr int kStages = 2;                   // of B and x; the state-only kernel has three (no C, no S)
-constexpr int kThreads = 640;
-constexpr int kStateWarps = 4, kDecayWarps = 4, kScoreWarps = 8;
-constexpr int kFirstDecay = kStateWarps, kFirstScore = kFirstDecay + kDecayWarps;
-constexpr int kIssueWarp = kFirstScore + kScoreWarps, kLoadWarp = kIssueWarp + 1,
-              kLoadCWarp = kLoadWarp + 1, kStoreWarp = kLoadCWarp + 1;
+constexpr int kStages = 3;                   // of x, which is y's place when it is done
+constexpr int kStateStages = 3;              // of B and x together, in the state-only kernel
+constexpr int kWorkers = 16;                 // warps that do the arithmetic
+constexpr int kIssueWarp = kWorkers, kLoadWarp = kWorkers + 1, kDecayWarp = kWorkers + 2;   // two decay warps
+constexpr int kThreads = 32 * (kWorkers + 4);
 constexpr uint32_t ATOM = 16384;             // [128 rows][64 columns] bf16, 128-byte swizzle
 constexpr uint32_t kTile = 2 * ATOM;
 
-// shared memory: per stage B, X; one C (free again after a chunk's second product); S as bf16 (rows = value
-// columns, K = N)
-constexpr uint32_t OFF_B = 0, OFF_X = kTile, kStageBytes = 2 * kTile;
-constexpr uint32_t OFF_C = kStages * kStageBytes, OFF_S = OFF_C + kTile;
+// shared memory: x, B, C, S as bf16 (rows = value columns, K = N)
+constexpr uint32_t OFF_X = 0, OFF_B = kStages * kTile, OFF_C = OFF_B + kTile, OFF_S = OFF_C + kTile;
 constexpr uint32_t SMEM_DYN = OFF_S + kTile + 1024;
+constexpr uint32_t kStageBytes = 2 * kTile;  // state-only kernel: B, then x
+static_assert(kStateStages * kStageBytes + 1024 <= SMEM_DYN, "the state-only kernel's stages fit");
 
-// tensor memory columns (the state-only kernel's three groups have their weighted x at TM_HI, TM_G and TM_Y)
-constexpr uint32_t TM_S = 0, TM_Y = 128, TM_G = 256, TM_HI = 384, TM_LO = 448, TM_COLS = 512;
+// tensor memory columns (the state-only kernel's three groups have their weighted x at TM_W, TM_G and TM_Y)
+constexpr uint32_t TM_S = 0, TM_Y = 128, TM_G = 256, TM_W = 384, TM_COLS = 512;
+constexpr uint32_t kUpper = 16u << 16;       // the second 16 lanes of a warp's quarter of the tensor memory
 
 struct __align__(16) Scalars {               // of one chunk, per head of the tile
     float neg[2][kTok];                      // -(running sum within the token's 32-token block, inclusive)
@@ -186,30 +190,8 @@ __device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t* u
                  "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
                  : "memory");
 }
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* u) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-                 "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
-                 : "memory");
-}
-
-// TMEM -> registers, 64 columns, complete on return.  Load and wait are one statement: between two, the
+// TMEM -> registers, 32 columns, complete on return.  Load and wait are one statement: between two, the
 // compiler may move or spill registers that the load has not written yet.
-__device__ __forceinline__ void tmem_read64(uint32_t taddr, float* r) {
-    uint32_t* u = reinterpret_cast<uint32_t*>(r);
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=&r"(u[0]), "=&r"(u[1]), "=&r"(u[2]), "=&r"(u[3]), "=&r"(u[4]), "=&r"(u[5]), "=&r"(u[6]), "=&r"(u[7]),
-          "=&r"(u[8]), "=&r"(u[9]), "=&r"(u[10]), "=&r"(u[11]), "=&r"(u[12]), "=&r"(u[13]), "=&r"(u[14]), "=&r"(u[15]),
-          "=&r"(u[16]), "=&r"(u[17]), "=&r"(u[18]), "=&r"(u[19]), "=&r"(u[20]), "=&r"(u[21]), "=&r"(u[22]), "=&r"(u[23]),
-          "=&r"(u[24]), "=&r"(u[25]), "=&r"(u[26]), "=&r"(u[27]), "=&r"(u[28]), "=&r"(u[29]), "=&r"(u[30]), "=&r"(u[31]),
-          "=&r"(u[32]), "=&r"(u[33]), "=&r"(u[34]), "=&r"(u[35]), "=&r"(u[36]), "=&r"(u[37]), "=&r"(u[38]), "=&r"(u[39]),
-          "=&r"(u[40]), "=&r"(u[41]), "=&r"(u[42]), "=&r"(u[43]), "=&r"(u[44]), "=&r"(u[45]), "=&r"(u[46]), "=&r"(u[47]),
-          "=&r"(u[48]), "=&r"(u[49]), "=&r"(u[50]), "=&r"(u[51]), "=&r"(u[52]), "=&r"(u[53]), "=&r"(u[54]), "=&r"(u[55]),
-          "=&r"(u[56]), "=&r"(u[57]), "=&r"(u[58]), "=&r"(u[59]), "=&r"(u[60]), "=&r"(u[61]), "=&r"(u[62]), "=&r"(u[63])
-        : "r"(taddr)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_read32(uint32_t taddr, float* r) {
     uint32_t* u = reinterpret_cast<uint32_t*>(r);
     asm volatile(
@@ -232,26 +214,26 @@ __device__ __forceinline__ void tmem_write32(uint32_t taddr, const float* r) {
           "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
         : "memory");
 }
-// Three runs of 16 columns, 32 apart, and a fourth at `other`.
-__device__ __forceinline__ void tmem_read3x16(uint32_t taddr, float* r, uint32_t other, float* r2) {
+// Four runs of 8 columns, 32 apart.
+__device__ __forceinline__ void tmem_read4x8(uint32_t taddr, float* r) {
     uint32_t* u = reinterpret_cast<uint32_t*>(r);
-    uint32_t* w = reinterpret_cast<uint32_t*>(r2);
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%64];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%65];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47}, [%66];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%67];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%33];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%34];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24, %25, %26, %27, %28, %29, %30, %31}, [%35];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=&r"(u[0]), "=&r"(u[1]), "=&r"(u[2]), "=&r"(u[3]), "=&r"(u[4]), "=&r"(u[5]), "=&r"(u[6]), "=&r"(u[7]),
           "=&r"(u[8]), "=&r"(u[9]), "=&r"(u[10]), "=&r"(u[11]), "=&r"(u[12]), "=&r"(u[13]), "=&r"(u[14]), "=&r"(u[15]),
           "=&r"(u[16]), "=&r"(u[17]), "=&r"(u[18]), "=&r"(u[19]), "=&r"(u[20]), "=&r"(u[21]), "=&r"(u[22]), "=&r"(u[23]),
-          "=&r"(u[24]), "=&r"(u[25]), "=&r"(u[26]), "=&r"(u[27]), "=&r"(u[28]), "=&r"(u[29]), "=&r"(u[30]), "=&r"(u[31]),
-          "=&r"(u[32]), "=&r"(u[33]), "=&r"(u[34]), "=&r"(u[35]), "=&r"(u[36]), "=&r"(u[37]), "=&r"(u[38]), "=&r"(u[39]),
-          "=&r"(u[40]), "=&r"(u[41]), "=&r"(u[42]), "=&r"(u[43]), "=&r"(u[44]), "=&r"(u[45]), "=&r"(u[46]), "=&r"(u[47]),
-          "=&r"(w[0]), "=&r"(w[1]), "=&r"(w[2]), "=&r"(w[3]), "=&r"(w[4]), "=&r"(w[5]), "=&r"(w[6]), "=&r"(w[7]),
-          "=&r"(w[8]), "=&r"(w[9]), "=&r"(w[10]), "=&r"(w[11]), "=&r"(w[12]), "=&r"(w[13]), "=&r"(w[14]), "=&r"(w[15])
-        : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(other)
+          "=&r"(u[24]), "=&r"(u[25]), "=&r"(u[26]), "=&r"(u[27]), "=&r"(u[28]), "=&r"(u[29]), "=&r"(u[30]), "=&r"(u[31])
+        : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
         : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t* u) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(u[0]), "r"(u[1]),
+                 "r"(u[2]), "r"(u[3])
+                 : "memory");
 }
 
 // Bounded waits that also end when another warp of the CTA has given up.
@@ -263,10 +245,10 @@ struct Waiter {
     __device__ __noinline__ bool slow(uint32_t a, uint32_t parity) const {
         const uint64_t t0 = global_timer_ns();
         for (;;) {
+            if (*abort_flag) return false;
 #pragma unroll 1
             for (int i = 0; i < 32; ++i)
                 if (mbar_try_wait(a, parity)) return true;
-            if (*abort_flag) return false;
             if (global_timer_ns() - t0 > timeout_ns) {
                 *abort_flag = 1;
                 report_status(status, KDA_ERR_TIMEOUT);
@@ -290,50 +272,47 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
     if (lane == 0) mbar_arrive(bar);
 }
 
-template <int N, int P, bool STATE_ONLY>
-__global__ void __launch_bounds__(kThreads, 1)
-kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
-                  const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_y, const Params p) {
-    constexpr int NH = P == 64 ? 2 : 1;      // heads per tile
-    constexpr int ST = STATE_ONLY ? 3 : kStages;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw_base = smem_u32(smem_raw);
-    uint8_t* sm = smem_raw + (((raw_base + 1023u) & ~1023u) - raw_base);
-    const uint32_t sb = smem_u32(sm);
-    __shared__ Scalars scal[STATE_ONLY ? 3 : 2];
-    __shared__ uint64_t full[ST], empty[ST], full_c, bar_scal[2], bar_g, bar_cs, bar_upd[3], bar_px, bar_state, bar_w, bar_wst[3],
-        bar_behind[3], bar_init, bar_q,
-        bar_yfree, bar_staged, yread[kStages], bar_drain;
-    __shared__ uint32_t tmem_base_s;
-    __shared__ volatile int abort_s;
-    __shared__ int seq_s, seg_s;
-    __shared__ float seg_total_s[2], behind_s[3][2];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int H = p.H;
+// The tokens and heads of a CTA.
+struct Job {
+    int unit, unit0, seq, seg, n_seg;        // unit: the sequence's segment; unit0: its first segment
+    int g, h0, h1;                           // group and heads (h1 == h0: no second head)
+    int tok0, len, chunks;                   // first token within the sequence, tokens, chunks
+    bool last;                               // the sequence's last segment
+    size_t start;                            // token 0 of the job on the token axis of x, dt and y
+    int row0, row_seq;                       // coordinates of the first chunk in the tensor maps
+};
 
-    // ---- which tokens and which heads
-    const int unit = blockIdx.x / p.tiles, tile = blockIdx.x % p.tiles;
-    const int rep = H / p.G;
-    const int per_group = (rep + NH - 1) / NH;
-    const int g = tile / per_group, h0 = g * rep + (tile % per_group) * NH;
-    const int h1 = NH == 2 && h0 + 1 < (g + 1) * rep ? h0 + 1 : h0;      // no partner: the same head again
-    int seq, seg, len_seq;
-    size_t start;                            // first token of the sequence on the token axis of x, dt and y
+// Block-wide (it has barriers).  False: the CTA has no job.
+template <int NH>
+__device__ __forceinline__ bool find_job(const Params& p, Job& job) {
+    __shared__ int seq_s, seg_s;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int tile = blockIdx.x % p.tiles;
+    job.unit = blockIdx.x / p.tiles;
+    const int rep = p.H / p.G, per_group = (rep + NH - 1) / NH;
+    job.g = tile / per_group;
+    job.h0 = job.g * rep + (tile % per_group) * NH;
+    job.h1 = NH == 2 && job.h0 + 1 < (job.g + 1) * rep ? job.h0 + 1 : job.h0;
+    const int seg_tokens = p.seg_chunks > 0 ? p.seg_chunks * kTok : 0x7fffffff;
+    int len_seq;
+    size_t start;
     if (p.cu_seqlens) {
         const bool valid = packed_offsets_valid(p.cu_seqlens, p.n_seq, p.T);
         if (!valid && tid == 0) report_status(p.status, KDA_ERR_INVALID_ARG);
+        job.seq = job.unit;
+        job.seg = 0;
         if (p.seg_chunks > 0) {
             // units in order: each sequence's segments (one for an empty sequence)
             if (tid == 0) seq_s = -1;
             __syncthreads();
-            if (warp == 0) {
+            if (tid < 32) {
                 int before = 0;
                 for (int base = 0; base < p.n_seq; base += 32) {
                     const int i = base + lane;
                     int n = 0;
                     if (i < p.n_seq) {
                         const int len = valid ? p.cu_seqlens[i + 1] - p.cu_seqlens[i] : 0;
-                        n = max(1, (len + p.seg_chunks * kTok - 1) / (p.seg_chunks * kTok));
+                        n = max(1, (len + seg_tokens - 1) / seg_tokens);
                     }
                     int incl = n;
 #pragma unroll
@@ -341,63 +320,190 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                         const int t = __shfl_up_sync(0xffffffffu, incl, off);
                         if (lane >= off) incl += t;
                     }
-                    if (unit >= before + incl - n && unit < before + incl) {
+                    if (job.unit >= before + incl - n && job.unit < before + incl) {
                         seq_s = i;
-                        seg_s = unit - (before + incl - n);
+                        seg_s = job.unit - (before + incl - n);
                     }
                     before += __shfl_sync(0xffffffffu, incl, 31);
-                    if (unit < before) break;
+                    if (job.unit < before) break;
                 }
             }
             __syncthreads();
-            seq = seq_s;
-            seg = seg_s;
-            if (seq < 0) return;             // the grid holds the most units that T tokens can make
-        } else {
-            seq = unit;
-            seg = 0;
+            job.seq = seq_s;
+            job.seg = seg_s;
+            if (job.seq < 0) return false;   // the grid holds the most units that T tokens can make
         }
-        start = valid ? (size_t)p.cu_seqlens[seq] : 0;
-        len_seq = valid ? p.cu_seqlens[seq + 1] - p.cu_seqlens[seq] : 0;
+        start = valid ? (size_t)p.cu_seqlens[job.seq] : 0;
+        len_seq = valid ? p.cu_seqlens[job.seq + 1] - p.cu_seqlens[job.seq] : 0;
+        job.row_seq = 0;
+        job.row0 = (int)start;
     } else {
-        seq = unit / p.segs;
-        seg = unit % p.segs;
-        start = (size_t)seq * p.T;
+        job.seq = job.unit / p.segs;
+        job.seg = job.unit % p.segs;
+        start = (size_t)job.seq * p.T;
         len_seq = p.T;
+        job.row_seq = job.seq;
+        job.row0 = 0;
     }
-    const int seg_tokens = p.seg_chunks > 0 ? p.seg_chunks * kTok : 0x7fffffff;
-    const int tok0 = seg * (p.seg_chunks * kTok);                        // first token within the sequence
-    const int len = min(len_seq - tok0, seg_tokens);
-    const bool last_seg = tok0 + len >= len_seq;
-    const int n_seg = p.seg_chunks > 0 ? max(1, (len_seq + seg_tokens - 1) / seg_tokens) : 1;
-    const int unit0 = unit - seg;            // the sequence's first segment
-    if (STATE_ONLY && last_seg) return;
-    const int chunks = (len + kTok - 1) / kTok;
-    const int row_seq = p.cu_seqlens ? 0 : seq;                          // batch coordinate of the tensor maps
-    const int row0 = (p.cu_seqlens ? (int)start : 0) + tok0;             // token coordinate of the first chunk
+    job.tok0 = job.seg * (p.seg_chunks * kTok);
+    job.row0 += job.tok0;
+    job.start = start + job.tok0;
+    job.len = min(len_seq - job.tok0, seg_tokens);
+    job.last = job.tok0 + job.len >= len_seq;
+    job.chunks = (job.len + kTok - 1) / kTok;
+    job.n_seg = p.seg_chunks > 0 ? max(1, (len_seq + seg_tokens - 1) / seg_tokens) : 1;
+    job.unit0 = job.unit - job.seg;
+    return true;
+}
 
+// The states of one value column (a lane of the warp, in its quarter of the tensor-memory lanes).
+template <int N, int P>
+struct Column {
+    static constexpr int NH = P == 64 ? 2 : 1;
+    const Params& p;
+    const Job& job;
+    int head, pc;
+    bool dup;                                // carried, not stored
+    size_t s_off;                            // S[seq][head][0][pc]
+
+    __device__ __forceinline__ Column(const Params& p_, const Job& job_, int col) : p(p_), job(job_) {
+        const int half = NH == 2 ? col >> 6 : 0;
+        head = half ? job.h1 : job.h0;
+        pc = NH == 2 ? col & 63 : col;
+        dup = NH == 2 && half == 1 && job.h1 == job.h0;
+        s_off = (((size_t)job.seq * p.H + head) * N) * P + pc;
+    }
+    __device__ __forceinline__ float* seg_state(int unit) const {
+        return p.seg_state + ((size_t)unit * p.H + head) * N * P + pc;
+    }
+    __device__ __forceinline__ void store(float* to, int n0, const float* v) const {
+        if (!dup) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) to[(size_t)(n0 + i) * P] = v[i];
+        }
+    }
+    __device__ __forceinline__ void load(const float* from, int n0, float* v) const {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = from ? from[(size_t)(n0 + i) * P] : 0.f;
+    }
+    // The start state of 32 rows n.  Sequences of several segments: the first launch starts segment 0 from S0,
+    // and leaves a copy of S0 in the last segment's place, which no local state takes; the second launch reads S0
+    // nowhere else, so that S_T may be S0.
+    __device__ __forceinline__ void load_start(int n0, float* v) const {
+        if (job.n_seg == 1) return load(p.S0 ? p.S0 + s_off : nullptr, n0, v);
+        load(seg_state(job.seg == 0 ? job.unit0 + job.n_seg - 1 : job.unit0), n0, v);
+#pragma unroll 1
+        for (int k = 1; k < job.seg; ++k) {
+            const float d = ex2(p.seg_decay[(size_t)(job.unit0 + k) * p.H + head]);
+            float l[32];
+            load(seg_state(job.unit0 + k), n0, l);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(d, v[i], l[i]);
+        }
+    }
+};
+
+// Sums over a block of 32 tokens, one to a lane: up to the token (inclusive), and after it.
+__device__ __forceinline__ void block_sums(float la, int lane, float& incl, float& after) {
+    float rev = la;
+    incl = la;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const float a = __shfl_up_sync(0xffffffffu, incl, off), b = __shfl_down_sync(0xffffffffu, rev, off);
+        if (lane >= off) incl += a;
+        if (lane + off < 32) rev += b;
+    }
+    const float next = __shfl_down_sync(0xffffffffu, rev, 1);
+    after = lane == 31 ? 0.f : next;
+}
+__device__ __forceinline__ void store_weight(Scalars& sc, int i, int j, float w) {
+    const __nv_bfloat16 w1 = __float2bfloat16_rn(w), w2 = __float2bfloat16_rn(w - __bfloat162float(w1));
+    sc.w1[i][j] = __bfloat16_as_ushort(w1);
+    sc.w2[i][j] = __bfloat16_as_ushort(w2);
+}
+// The weighted x of 32 tokens (groups of 8 from tg0 on) and a warp's 32 value columns, hi and lo, into the tensor
+// memory at `place` (lanes = value columns, columns = pairs of tokens).
+__device__ __forceinline__ void weigh_x(uint32_t place, const Scalars& sc, int half, uint32_t x_tile, int quarter,
+                                        int lane, int tg0) {
+    const uint32_t xa = x_tile + (quarter >> 1) * ATOM + (lane & 7) * 128 +
+                        (((uint32_t)((quarter & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
+    const uint32_t* w1 = reinterpret_cast<const uint32_t*>(sc.w1[half]) + (lane & 3);
+    const uint32_t* w2 = reinterpret_cast<const uint32_t*>(sc.w2[half]) + (lane & 3);
+    uint32_t hi[2][8], lo[2][8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t x[4];
+        ldmatrix4t(xa + (tg0 + k) * 1024, x);
+        const uint32_t a = w1[4 * (tg0 + k)], b = w2[4 * (tg0 + k)];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const uint32_t h = mul_bf16x2(x[m], a);
+            hi[m >> 1][2 * k + (m & 1)] = h;
+            lo[m >> 1][2 * k + (m & 1)] = fma_bf16x2(x[m], b, fma_bf16x2(x[m], a, h ^ 0x80008000u));
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        tmem_st_16x128(place + 4 * tg0 + u * kUpper, hi[u]);
+        tmem_st_16x128(place + 4 * tg0 + u * kUpper + 64, lo[u]);
+    }
+}
+
+// Loads of a chunk's x and B.
+template <int NH>
+__device__ __forceinline__ void load_x(uint8_t* to, const CUtensorMap* tm_x, uint64_t* full, const Job& job, int row) {
+    for (int i = 0; i < 2; ++i)
+        tma_load_4d(to + i * ATOM, tm_x, full, NH == 2 ? 0 : 64 * i, NH == 2 && i ? job.h1 : job.h0, row, job.row_seq);
+}
+template <int N>
+__device__ __forceinline__ void load_bc(uint8_t* to, const CUtensorMap* tm, uint64_t* full, const Job& job, int row) {
+    for (int i = 0; i < N / 64; ++i) tma_load_4d(to + i * ATOM, tm, full, 64 * i, job.g, row, job.row_seq);
+}
+template <int N>
+__device__ __forceinline__ void prefetch_bc(const CUtensorMap* tm, const Job& job, int row) {
+    for (int i = 0; i < N / 64; ++i) tma_prefetch_4d(tm, 64 * i, job.g, row, job.row_seq);
+}
+template <int NH>
+__device__ __forceinline__ void prefetch_x(const CUtensorMap* tm_x, const Job& job, int row) {
+    for (int i = 0; i < 2; ++i)
+        tma_prefetch_4d(tm_x, NH == 2 ? 0 : 64 * i, NH == 2 && i ? job.h1 : job.h0, row, job.row_seq);
+}
+
+// ------------------------------------------------------------------ states of the segments
+
+constexpr int kStateThreads = 32 * 18;       // 0-3 the end; 4-15 three groups, each every third chunk; 16 products, 17 loads
+
+template <int N, int P>
+__global__ void __launch_bounds__(kStateThreads, 1)
+kda_ssm_state_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b, const Params p) {
+    constexpr int NH = P == 64 ? 2 : 1, ST = kStateStages;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_base = smem_u32(smem_raw);
+    uint8_t* sm = smem_raw + (((raw_base + 1023u) & ~1023u) - raw_base);
+    const uint32_t sb = smem_u32(sm);
+    __shared__ Scalars scal[ST];
+    __shared__ uint64_t full[ST], empty[ST], bar_w[ST], bar_upd[ST], bar_behind[ST], bar_total, bar_drain;
+    __shared__ float behind_s[ST][2], total_s[2];
+    __shared__ uint32_t tmem_base_s;
+    __shared__ volatile int abort_s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3;
+    Job job;
+    if (!find_job<NH>(p, job) || job.last) return;
+    const int chunks = job.chunks;           // all whole
     if (tid == 0) {
-        for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-        for (int i = 0; i < kStages; ++i) mbar_init(&yread[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&bar_scal[i], kDecayWarps);
-        mbar_init(&full_c, 1);
-        mbar_init(&bar_g, 1);
-        mbar_init(&bar_init, N / 8);
-        mbar_init(&bar_cs, 1);
-        for (int i = 0; i < 3; ++i) mbar_init(&bar_upd[i], 1);
-        mbar_init(&bar_px, 1);
-        static_assert(kStateWarps == kDecayWarps, "bar_state counts either");
-        mbar_init(&bar_state, kStateWarps);
-        mbar_init(&bar_yfree, kScoreWarps);
-        mbar_init(&bar_staged, kScoreWarps);
-        mbar_init(&bar_w, kDecayWarps);
-        for (int i = 0; i < 3; ++i) { mbar_init(&bar_wst[i], kDecayWarps); mbar_init(&bar_behind[i], kDecayWarps); }
-        mbar_init(&bar_q, kScoreWarps);
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+            mbar_init(&bar_w[i], 4);
+            mbar_init(&bar_upd[i], 1);
+            mbar_init(&bar_behind[i], 4);
+        }
+        mbar_init(&bar_total, 4);
         mbar_init(&bar_drain, 1);
         fence_mbar_init();
         abort_s = 0;
-        prefetch_tensormap(&tm_x); prefetch_tensormap(&tm_b); prefetch_tensormap(&tm_c);
-        prefetch_tensormap(&tm_y);
+        prefetch_tensormap(&tm_x);
+        prefetch_tensormap(&tm_b);
     }
     if (warp == 0) {
         tmem_alloc(&tmem_base_s, TM_COLS);
@@ -408,113 +514,232 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     tc_fence_after_sync();
     const uint32_t tbase = tmem_base_s;
     const Waiter wait{&abort_s, p.status, p.timeout_ns};
-    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;            // this warp's tensor-memory lanes
-    const int quarter = warp & 3;
+    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    auto row_of = [&](int c) { return job.row0 + (chunks - 1 - c) * kTok; };   // from the last chunk to the first
 
-    // ---- states: a lane of a warp is one value column, in the warp's quarter of the tensor-memory lanes
-    const int col = 32 * quarter + lane;                                // value column of this lane
-    const int half = NH == 2 ? col >> 6 : 0;
-    const int head = half ? h1 : h0, pc = NH == 2 ? col & 63 : col;
-    const bool dup = NH == 2 && half == 1 && h1 == h0;               // carried, not stored
-    const size_t s_off = (((size_t)seq * H + head) * N) * P + pc;    // S[seq][head][0][pc]
-    auto seg_state = [&](int u) { return p.seg_state + ((size_t)u * H + head) * N * P + pc; };
-    auto store_state = [&](float* to, int n0, const float* v) {
-        if (!dup) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) to[(size_t)(n0 + i) * P] = v[i];
-        }
-    };
-    // The start state of 32 rows n.  Sequences of several segments: the first launch starts segment 0 from
-    // S0, and leaves a copy of S0 in the last segment's place, which no local state takes; the second launch
-    // reads S0 nowhere else, so that S_T may be S0.
-    auto load_start = [&](int n0, float* v) {
-        const float* from = STATE_ONLY || n_seg == 1 ? (p.S0 && seg == 0 ? p.S0 + s_off : nullptr)
-                                                     : seg_state(seg == 0 ? unit0 + n_seg - 1 : unit0);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = from ? from[(size_t)(n0 + i) * P] : 0.f;
-        if constexpr (STATE_ONLY) {
-            if (seg == 0) store_state(seg_state(unit0 + n_seg - 1), n0, v);
-        } else {
-#pragma unroll 2
-            for (int k = 1; k < seg; ++k) {
-                const float d = ex2(p.seg_decay[(size_t)(unit0 + k) * H + head]);
-                const float* l = seg_state(unit0 + k);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = fmaf(d, v[i], l[(size_t)(n0 + i) * P]);
-            }
-        }
-    };
-    // 32 rows to each group of four warps, in parallel (each start state is as many dependent reads as segments)
-    if (!STATE_ONLY && warp < kIssueWarp && 8 * (warp & ~3) < N) {
-        const int n0 = 8 * (warp & ~3);
-        float v[32];
-        load_start(n0, v);
-        if (chunks > 0) {
-            tmem_write32(tbase + TM_S + lanes + n0, v);
-            tmem_wait_st();
-            tc_fence_before_sync();
-            warp_arrive(&bar_init, lane);
-        } else if (p.ST) {
-            store_state(p.ST + s_off, n0, v);            // an empty sequence
-        }
-    }
-    if (warp == kLoadWarp) {
-        // ------------------------------------------------------------ loads of B and x
+    if (warp == 17) {
         if (lane == 0) {
             int issued = 0;
             for (int c = 0; c < chunks; ++c) {
-                const int st = c % ST, t = row0 + (STATE_ONLY ? chunks - 1 - c : c) * kTok;
-                uint8_t* s = sm + st * kStageBytes;
-                // the stage is free after the last product of its last turn and once its y has been read out
-                if (c >= ST && (!wait.one(&empty[st], (uint32_t)(c / ST - 1) & 1) ||
-                                (!STATE_ONLY && !wait.one(&yread[st % kStages], (uint32_t)(c / ST - 1) & 1))))
-                    break;
-                mbar_arrive_expect_tx(&full[st], ATOM * (2 + N / 64));
-                for (int i = 0; i < N / 64; ++i) tma_load_4d(s + OFF_B + i * ATOM, &tm_b, &full[st], 64 * i, g, t, row_seq);
-                for (int i = 0; i < 2; ++i)
-                    tma_load_4d(s + OFF_X + i * ATOM, &tm_x, &full[st], NH == 2 ? 0 : 64 * i, NH == 2 && i ? h1 : h0, t, row_seq);
+                if (c >= ST && !wait.one(&empty[c % ST], (uint32_t)(c / ST - 1) & 1)) break;
+                uint8_t* stage = sm + (c % ST) * kStageBytes;
+                mbar_arrive_expect_tx(&full[c % ST], ATOM * (2 + N / 64));
+                load_bc<N>(stage, &tm_b, &full[c % ST], job, row_of(c));
+                load_x<NH>(stage + kTile, &tm_x, &full[c % ST], job, row_of(c));
                 ++issued;
-                // x of the stage's next turn, which no other CTA reads, into L2 (3% at P = 128)
-                if (c + ST < chunks)
-                    for (int i = 0; i < 2; ++i)
-                        tma_prefetch_4d(&tm_x, NH == 2 ? 0 : 64 * i, NH == 2 && i ? h1 : h0,
-                                        STATE_ONLY ? t - ST * kTok : t + ST * kTok, row_seq);
+                if (c + ST < chunks) prefetch_x<NH>(&tm_x, job, row_of(c + ST));
             }
             // nothing may be in flight when the CTA exits
             for (int c = max(0, issued - ST); c < issued; ++c)
-                if (!mbar_wait(&full[c % ST], (uint32_t)(c / ST) & 1, p.timeout_ns))
-                    report_status(p.status, KDA_ERR_TIMEOUT);
+                if (!mbar_wait(&full[c % ST], (uint32_t)(c / ST) & 1, p.timeout_ns)) report_status(p.status, KDA_ERR_TIMEOUT);
         }
-    } else if (warp == kLoadCWarp) {
-        // ------------------------------------------------------------ loads of C, each as soon as the last is used up
-        if (lane == 0 && !STATE_ONLY) {
-            int issued = 0;
+    } else if (warp == 16) {
+        if (lane == 0) {
+            const uint32_t id_up = idesc_bf16_f32(128, N, false, true);
             for (int c = 0; c < chunks; ++c) {
-                if (c > 0 && !wait.one(&bar_cs, (uint32_t)(c - 1) & 1)) break;
-                mbar_arrive_expect_tx(&full_c, kTile / 128 * N);
-                for (int i = 0; i < N / 64; ++i)
-                    tma_load_4d(sm + OFF_C + i * ATOM, &tm_c, &full_c, 64 * i, g, row0 + c * kTok, row_seq);
-                ++issued;
+                const uint32_t b_tile = sb + (c % ST) * kStageBytes, w = tbase + TM_W - 128 * (c % ST);
+                if (!wait.one(&bar_w[c % ST], (uint32_t)(c / ST) & 1)) break;
+                tc_fence_after_sync();
+                issue_ts(tbase + TM_S, w, b_tile, id_up, c > 0);
+                issue_ts(tbase + TM_S, w + 64, b_tile, id_up, true);
+                mma_commit(&bar_upd[c % ST]);
+                mma_commit(&empty[c % ST]);
             }
-            if (issued > 0 && !mbar_wait(&full_c, (uint32_t)(issued - 1) & 1, p.timeout_ns))
-                report_status(p.status, KDA_ERR_TIMEOUT);
+            mma_commit(&bar_drain);
+            if (!mbar_wait(&bar_drain, 0, p.timeout_ns)) report_status(p.status, KDA_ERR_TIMEOUT);
         }
-    } else if (warp == kStoreWarp) {
-        // ------------------------------------------------------------ stores of y from the x tiles
-        if (lane == 0 && !STATE_ONLY) {
-            for (int c = 0; c < chunks; ++c) {
+    } else if (warp < 4) {
+        // the segment's state: the sum of its chunks, and for the first segment what is left of S0
+        const Column<N, P> col(p, job, 32 * quarter + lane);
+        bool ok = wait.warp(&bar_total, 0) && wait.warp(&bar_upd[(chunks - 1) % ST], (uint32_t)((chunks - 1) / ST) & 1);
+        tc_fence_after_sync();
+        const float decay = ex2(total_s[NH == 2 ? quarter >> 1 : 0]);
+#pragma unroll 1
+        for (int n0 = 0; n0 < N && ok; n0 += 32) {
+            float v[32], start[32];
+            tmem_read32(tbase + TM_S + lanes + n0, v);
+            if (job.seg == 0) {
+                col.load(p.S0 ? p.S0 + col.s_off : nullptr, n0, start);
+                col.store(col.seg_state(job.unit0 + job.n_seg - 1), n0, start);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = fmaf(decay, start[i], v[i]);
+            }
+            col.store(col.seg_state(job.unit), n0, v);
+        }
+    } else {
+        const int group = (warp >> 2) - 1, j = 32 * quarter + lane;
+        float rate[NH], bias[NH], raw[NH], behind[NH];
+#pragma unroll
+        for (int i = 0; i < NH; ++i) {
+            const int head = i ? job.h1 : job.h0;
+            rate[i] = p.A[head] * 1.4426950408889634f;                   // decays in powers of two
+            bias[i] = p.dt_bias ? p.dt_bias[head] : 0.f;
+            behind[i] = 0.f;
+        }
+        auto load_dt = [&](int c) {
+#pragma unroll
+            for (int i = 0; i < NH; ++i)
+                raw[i] = load_elem(p.dt, (job.start + (size_t)(chunks - 1 - c) * kTok + j) * p.lddt + (i ? job.h1 : job.h0));
+        };
+        if (group < chunks) load_dt(group);
+        bool ok = true;
+        for (int c = group; c < chunks; c += ST) {
+            Scalars& sc = scal[group];
+            float after[NH], stp[NH];
+#pragma unroll
+            for (int i = 0; i < NH; ++i) {
+                stp[i] = softplus(raw[i] + bias[i]);
+                float incl;
+                block_sums(stp[i] * rate[i], lane, incl, after[i]);
+                if (lane == 31) sc.total[i][quarter] = incl;
+            }
+            if (c + ST < chunks) load_dt(c + ST);
+            named_bar_sync(1 + 2 * group, 128);
+            // the decay behind the chunk, handed on from group to group
+            if (c > 0) (void)wait.warp(&bar_behind[group], (uint32_t)((c - 1) / ST) & 1);
+            const int next = (group + 1) % ST;
+#pragma unroll
+            for (int i = 0; i < NH; ++i) {
+                behind[i] = c > 0 ? behind_s[group][i] : 0.f;
+                float rest = after[i] + behind[i], all = behind[i];
+#pragma unroll
+                for (int b = 3; b >= 0; --b) {
+                    if (b > quarter) rest += sc.total[i][b];
+                    all += sc.total[i][b];
+                }
+                store_weight(sc, i, j, stp[i] * ex2(rest));
+                behind[i] = all;
+                if (j == 0) behind_s[next][i] = all;
+            }
+            warp_arrive(&bar_behind[next], lane);
+            ok = wait.warp(&full[c % ST], (uint32_t)(c / ST) & 1) &&
+                 (c < ST || wait.warp(&bar_upd[group], (uint32_t)(c / ST - 1) & 1));   // the operand's place is free
+            ok = named_bar_and(2 + 2 * group, 128, ok);                  // w of all tokens; the four warps leave together
+            if (!ok) break;
+            tc_fence_after_sync();
+#pragma unroll 1
+            for (int tg = 0; tg < 16; tg += 4)
+                weigh_x(tbase + lanes + TM_W - 128 * group, sc, NH == 2 ? quarter >> 1 : 0, sb + group * kStageBytes + kTile,
+                        quarter, lane, tg);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            warp_arrive(&bar_w[group], lane);
+        }
+        if (group == (chunks - 1) % ST) {
+            if (ok && j == 0) {
+                p.seg_decay[(size_t)job.unit * p.H + job.h0] = total_s[0] = behind[0];
+                if (NH == 2 && job.h1 != job.h0) p.seg_decay[(size_t)job.unit * p.H + job.h1] = behind[NH - 1];
+                total_s[1] = behind[NH - 1];
+            }
+            warp_arrive(&bar_total, lane);
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == 0) tmem_dealloc(tbase, TM_COLS);
+}
+
+// ------------------------------------------------------------------ outputs and states
+
+template <int N, int P>
+__global__ void __launch_bounds__(kThreads, 1)
+kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_b,
+                  const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_y, const Params p) {
+    constexpr int NH = P == 64 ? 2 : 1;      // heads per tile
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_base = smem_u32(smem_raw);
+    uint8_t* sm = smem_raw + (((raw_base + 1023u) & ~1023u) - raw_base);
+    const uint32_t sb = smem_u32(sm);
+    __shared__ Scalars scal[2];
+    __shared__ uint64_t full_x[kStages], full_bc, bar_scal[2], scal_free[2], bar_g, bar_cs, bar_upd, bar_px,
+        bar_state, bar_w, bar_q, bar_yfree, bar_staged, bar_drain;
+    __shared__ uint32_t tmem_base_s;
+    __shared__ volatile int abort_s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3;
+    Job job;
+    if (!find_job<NH>(p, job)) return;
+    const int chunks = job.chunks;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(&full_x[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar_scal[i], NH);
+            mbar_init(&scal_free[i], kWorkers);
+        }
+        mbar_init(&full_bc, 1);
+        mbar_init(&bar_drain, 1);
+        mbar_init(&bar_g, 1);
+        mbar_init(&bar_cs, 1);
+        mbar_init(&bar_upd, 1);
+        mbar_init(&bar_px, 1);
+        mbar_init(&bar_state, kWorkers);
+        mbar_init(&bar_w, kWorkers);
+        mbar_init(&bar_q, kWorkers);
+        mbar_init(&bar_yfree, kWorkers);
+        mbar_init(&bar_staged, kWorkers);
+        fence_mbar_init();
+        abort_s = 0;
+        prefetch_tensormap(&tm_x); prefetch_tensormap(&tm_b); prefetch_tensormap(&tm_c); prefetch_tensormap(&tm_y);
+    }
+    if (warp == 0) {
+        tmem_alloc(&tmem_base_s, TM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tbase = tmem_base_s;
+    const Waiter wait{&abort_s, p.status, p.timeout_ns};
+
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------------------ loads of x and B, stores of y from the x tiles
+        if (lane == 0) {
+            int xs = 0, bs = 0;                                          // loads issued
+            auto x_in = [&](int c) {
+                if (c >= chunks) return;
                 const int st = c % kStages;
-                if (!wait.one(&bar_staged, c & 1)) break;
-                if (!p.cu_seqlens || len - c * kTok >= kTok) {           // whole tiles, clipped at the end of the tensor
+                mbar_arrive_expect_tx(&full_x[st], kTile);
+                load_x<NH>(sm + OFF_X + st * kTile, &tm_x, &full_x[st], job, job.row0 + c * kTok);
+                ++xs;
+                // x of the stage's next turn, which no other CTA reads, into L2
+                if (c + kStages < chunks) prefetch_x<NH>(&tm_x, job, job.row0 + (c + kStages) * kTok);
+            };
+            auto y_out = [&](int c) {
+                if (!wait.one(&bar_staged, c & 1)) return false;
+                if (!p.cu_seqlens || job.len - c * kTok >= kTok) {       // whole tiles, clipped at the end of the tensor
                     for (int i = 0; i < 2; ++i)
-                        if (!(NH == 2 && i == 1 && h1 == h0))
-                            tma_store_4d(&tm_y, sm + st * kStageBytes + OFF_X + i * ATOM, NH == 2 ? 0 : 64 * i,
-                                         NH == 2 && i ? h1 : h0, row0 + c * kTok, row_seq);
+                        if (!(NH == 2 && i == 1 && job.h1 == job.h0))
+                            tma_store_4d(&tm_y, sm + OFF_X + (c % kStages) * kTile + i * ATOM, NH == 2 ? 0 : 64 * i,
+                                         NH == 2 && i ? job.h1 : job.h0, job.row0 + c * kTok, job.row_seq);
                     bulk_commit_group();
                     bulk_wait_read_all();
                 }
-                mbar_arrive(&yread[st]);
+                return true;
+            };
+            for (int c = 0; c < kStages - 1; ++c) x_in(c);
+            bool ok = true;
+            for (int c = 0; c < chunks; ++c) {
+                // B and C are used up once the chunk before has updated the state (and all products before that have run)
+                if (c > 0 && !(ok = wait.one(&bar_upd, (uint32_t)(c - 1) & 1))) break;
+                mbar_arrive_expect_tx(&full_bc, 2 * kTile / 128 * N);
+                load_bc<N>(sm + OFF_B, &tm_b, &full_bc, job, job.row0 + c * kTok);
+                load_bc<N>(sm + OFF_C, &tm_c, &full_bc, job, job.row0 + c * kTok);
+                if (c + 1 < chunks) {
+                    prefetch_bc<N>(&tm_b, job, job.row0 + (c + 1) * kTok);
+                    prefetch_bc<N>(&tm_c, job, job.row0 + (c + 1) * kTok);
+                }
+                ++bs;
+                // a tile's next x follows once the y formed in its place has been read out
+                if (c > 0 && !(ok = y_out(c - 1))) break;
+                x_in(c + kStages - 1);
             }
+            if (ok && chunks > 0) (void)y_out(chunks - 1);
+            // nothing may be in flight when the CTA exits
+            bool done = bs == 0 || mbar_wait(&full_bc, (uint32_t)(bs - 1) & 1, p.timeout_ns);
+            for (int c = max(0, xs - kStages); c < xs; ++c)
+                done = mbar_wait(&full_x[c % kStages], (uint32_t)(c / kStages) & 1, p.timeout_ns) && done;
+            if (!done) report_status(p.status, KDA_ERR_TIMEOUT);
             bulk_wait_all();
         }
     } else if (warp == kIssueWarp) {
@@ -524,364 +749,252 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             const uint32_t id_cs = idesc_bf16_f32(128, kCols, false, false);
             const uint32_t id_px = idesc_bf16_f32(128, P, false, true);
             const uint32_t id_up = idesc_bf16_f32(128, N, false, true);
-            auto issue_g = [&](int c) {
-                if (!wait.one(&full[c % kStages], (uint32_t)(c / kStages) & 1) || !wait.one(&full_c, c & 1)) return false;
+            for (int c = 0; c < chunks; ++c) {
+                const uint32_t par = c & 1;
+                // products run in order: G takes the place that Q X of the chunk before has read
+                if (!wait.one(&full_bc, par)) break;
                 tc_fence_after_sync();
-                issue_ss<N>(tbase + TM_G, sb + OFF_C, sb + (c % kStages) * kStageBytes + OFF_B, id_g);
+                issue_ss<N>(tbase + TM_G, sb + OFF_C, sb + OFF_B, id_g);
                 mma_commit(&bar_g);
-                return true;
-            };
-            bool ok = STATE_ONLY || chunks == 0 || issue_g(0);
-            if constexpr (STATE_ONLY) {
-                for (int c = 0; c < chunks; ++c) {
-                    const uint32_t s = sb + (c % ST) * kStageBytes, w = tbase + TM_HI - 128 * (c % ST);
-                    if (!wait.one(&bar_wst[c % ST], (uint32_t)(c / ST) & 1)) break;
-                    tc_fence_after_sync();
-                    issue_ts(tbase + TM_S, w, s + OFF_B, id_up, c > 0);
-                    issue_ts(tbase + TM_S, w + 64, s + OFF_B, id_up, true);
-                    mma_commit(&bar_upd[c % ST]);
-                    mma_commit(&empty[c % ST]);
-                }
-                ok = false;
-            }
-            for (int c = 0; c < chunks && ok; ++c) {
-                const uint32_t s = sb + (c % kStages) * kStageBytes, par = c & 1;
-                ok = wait.one(&bar_state, par);          // S as bf16 and decayed
-                if (ok && !STATE_ONLY && c > 0) ok = wait.one(&bar_yfree, par ^ 1);
-                if (!ok) break;
+                if (!wait.one(&bar_state, par) || !wait.one(&bar_w, par)) break;   // S decayed and as bf16; the weighted x
                 tc_fence_after_sync();
-                if (!STATE_ONLY) {
-                    issue_ss<N>(tbase + TM_Y, sb + OFF_C, sb + OFF_S, id_cs);
-                    mma_commit(&bar_cs);
-                }
-                ok = wait.one(&bar_w, par);              // weighted x
-                if (!ok) break;
+                issue_ts(tbase + TM_S, tbase + TM_W, sb + OFF_B, id_up, true);
+                if (c > 0 && !wait.one(&bar_yfree, par ^ 1)) break;      // Y is free
                 tc_fence_after_sync();
-                issue_ts(tbase + TM_S, tbase + TM_HI, s + OFF_B, id_up, true);
-                if (!STATE_ONLY) {
-                    ok = wait.one(&bar_q, par);          // Q, and Y scaled
-                    if (!ok) break;
-                    tc_fence_after_sync();
+                issue_ss<N>(tbase + TM_Y, sb + OFF_C, sb + OFF_S, id_cs);
+                mma_commit(&bar_cs);
+                issue_ts(tbase + TM_S, tbase + TM_W + 64, sb + OFF_B, id_up, true);
+                mma_commit(&bar_upd);
+                if (!wait.one(&bar_q, par)) break;                       // Q, and Y scaled
+                tc_fence_after_sync();
 #pragma unroll
-                    for (int i = 0; i < NH; ++i)
-                        issue_ts(tbase + TM_Y + i * P, tbase + TM_G + 64 * i, s + OFF_X + (NH == 2 ? i * ATOM : 0), id_px, true);
-                    mma_commit(&bar_px);
-                }
-                issue_ts(tbase + TM_S, tbase + TM_LO, s + OFF_B, id_up, true);
-                mma_commit(&bar_upd[0]);
-                mma_commit(&empty[c % kStages]);
-                if (!STATE_ONLY && c + 1 < chunks) ok = issue_g(c + 1);
+                for (int i = 0; i < NH; ++i)
+                    issue_ts(tbase + TM_Y + i * P, tbase + TM_G + 64 * i,
+                             sb + OFF_X + (c % kStages) * kTile + (NH == 2 ? i * ATOM : 0), id_px, true);
+                mma_commit(&bar_px);
             }
             mma_commit(&bar_drain);
             if (!mbar_wait(&bar_drain, 0, p.timeout_ns)) report_status(p.status, KDA_ERR_TIMEOUT);
         }
-    } else if (warp < kStateWarps) {
-        // ------------------------------------------------------------ state
-        bool ok = true;
-        for (int c = 0; !STATE_ONLY && c < chunks && ok; ++c) {
-            const uint32_t par = c & 1;
-            const Scalars& sc = scal[c & 1];
-            ok = wait.warp(&bar_scal[c & 1], (c >> 1) & 1) &&
-                 (c == 0 ? wait.warp(&bar_init, 0) : wait.warp(&bar_upd[0], par ^ 1));
-            if (!ok) break;
-            tc_fence_after_sync();
-            const float decay = ex2((sc.total[half][0] + sc.total[half][1]) + (sc.total[half][2] + sc.total[half][3]));
-            // S: its bf16 copy for this chunk's read-out, then decayed to the chunk's end for the update
-#pragma unroll 1
-            for (int n0 = 0; n0 < N; n0 += 64) {
-                float v[64];
-                const uint32_t ta = tbase + TM_S + lanes + n0;
-                tmem_read64(ta, v);
+    } else if (warp >= kDecayWarp) {
+        // ------------------------------------------------------------ decays, up to two chunks ahead: a head to each warp, or
+        // every other chunk
+        const float rate0 = p.A[job.h0] * 1.4426950408889634f, rate1 = p.A[job.h1] * 1.4426950408889634f;   // powers of two
+        const float bias0 = p.dt_bias ? p.dt_bias[job.h0] : 0.f, bias1 = p.dt_bias ? p.dt_bias[job.h1] : 0.f;
+        const unsigned short* dt = reinterpret_cast<const unsigned short*>(p.dt) + job.start * p.lddt;
+        unsigned short raw[4];                                           // token 32 k + lane; converted when used
+        auto load_dt = [&](int n) {
 #pragma unroll
-                for (int i = 0; i < 64; i += 8)
-                    *reinterpret_cast<uint4*>(sm + OFF_S + sw128_offset(col, n0 + i, ATOM)) =
+            for (int k = 0; k < 4; ++k) {
+                const int t = n / NH * kTok + 32 * k + lane;
+                raw[k] = t < job.len ? dt[t * p.lddt + (n % NH ? job.h1 : job.h0)] : (unsigned short)0;
+            }
+        };
+        load_dt(warp - kDecayWarp);
+        for (int n = warp - kDecayWarp; n < chunks * NH; n += 2) {
+            const int c = n / NH, i = n % NH;
+            const float rate = i ? rate1 : rate0, bias = i ? bias1 : bias0;
+            float step[4], incl[4], after[4], total[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                step[k] = c * kTok + 32 * k + lane < job.len
+                              ? softplus(__bfloat162float(__ushort_as_bfloat16(raw[k])) + bias) : 0.f;
+                block_sums(step[k] * rate, lane, incl[k], after[k]);
+                total[k] = __shfl_sync(0xffffffffu, incl[k], 31);
+            }
+            load_dt(n + 2);
+            if (c >= 2 && !wait.warp(&scal_free[c & 1], (uint32_t)(c / 2 - 1) & 1)) break;
+            Scalars& sc = scal[c & 1];
+            float behind = 0.f;                                          // the blocks after this one
+#pragma unroll
+            for (int k = 3; k >= 0; --k) {
+                const int j = 32 * k + lane;
+                sc.neg[i][j] = -incl[k];
+                sc.step[i][j] = step[k];
+                sc.col[i][j] = step[k] * ex2(after[k]);
+                store_weight(sc, i, j, step[k] * ex2(after[k] + behind));
+                behind += total[k];
+                if (lane == 0) sc.total[i][k] = total[k];
+            }
+            warp_arrive(&bar_scal[c & 1], lane);
+        }
+    } else {
+        // ------------------------------------------------------------ the arithmetic, by sixteen warps
+        // A warp works on the tensor-memory lanes of its quarter; the four parts share the columns.  After a wait that
+        // ran out it goes on to its end with whatever is there (the others count on it at the named barriers); nothing
+        // is stored then.
+        const int part = warp >> 2;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        const int r = 32 * quarter + lane;                               // value column of S^T, token of Y, G and Q
+        const int half = NH == 2 ? quarter >> 1 : 0;                     // head of this warp's value columns of S^T
+        const int yhead = NH == 2 ? part >> 1 : 0;                       // head of this warp's columns of Y
+        const Column<N, P> col(p, job, r);
+        const bool has_rows = 32 * part < N;                             // of S: 32 rows to a part
+        if (has_rows) {
+            float v[32];
+            col.load_start(32 * part, v);
+            if (chunks > 0) tmem_write32(tbase + TM_S + lanes + 32 * part, v);
+            else if (p.ST) col.store(p.ST + col.s_off, 32 * part, v);    // an empty sequence
+        }
+        tmem_wait_st();
+        const float skip0 = p.D ? p.D[job.h0] : 0.f, skip1 = p.D ? p.D[job.h1] : 0.f;
+        // the chunk's weighted x, 32 tokens to a part
+        auto weigh = [&](int c) {
+            (void)wait.warp(&bar_scal[c & 1], (uint32_t)(c >> 1) & 1);
+            (void)wait.warp(&full_x[c % kStages], (uint32_t)(c / kStages) & 1);
+            const uint32_t x_off = OFF_X + (c % kStages) * kTile;
+            const int n_valid = job.len - c * kTok;
+            if (p.cu_seqlens && n_valid < kTok) {
+                // rows of other sequences, or of none: zeros, so that nothing of theirs enters a sum
+                (void)wait.warp(&full_bc, c & 1);
+                if (r >= n_valid && (part < 2 || part - 2 < N / 64)) {
+                    uint8_t* row = sm + (part < 2 ? x_off + part * ATOM : OFF_B + (part - 2) * ATOM) + r * 128;
+                    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(row + i * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
+                named_bar_sync(3, 32 * kWorkers);
+            }
+            tc_fence_after_sync();
+            weigh_x(tbase + lanes + TM_W, scal[c & 1], half, sb + x_off, quarter, lane, 4 * part);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            warp_arrive(&bar_w, lane);
+        };
+        // S: its bf16 copy for the chunk's read-out, then decayed to the chunk's end for the update
+        auto carry = [&](int c) {
+            const Scalars& sc = scal[c & 1];
+            if (has_rows) {
+                const float decay = ex2((sc.total[half][0] + sc.total[half][1]) + (sc.total[half][2] + sc.total[half][3]));
+                float v[32];
+                const uint32_t ta = tbase + TM_S + lanes + 32 * part;
+                tmem_read32(ta, v);
+#pragma unroll
+                for (int i = 0; i < 32; i += 8)
+                    *reinterpret_cast<uint4*>(sm + OFF_S + sw128_offset(r, 32 * part + i, ATOM)) =
                         make_uint4(bf16x2(v[i], v[i + 1]), bf16x2(v[i + 2], v[i + 3]), bf16x2(v[i + 4], v[i + 5]),
                                    bf16x2(v[i + 6], v[i + 7]));
-                scale_by<64>(v, decay);
+                scale_by<32>(v, decay);
                 tmem_write32(ta, v);
-                tmem_write32(ta + 32, v + 32);
-            }
-            tmem_wait_st();
-            fence_proxy_async_smem();
-            tc_fence_before_sync();
-            if (!(p.skip_handoff && c == 0)) warp_arrive(&bar_state, lane);
-        }
-        if constexpr (STATE_ONLY) {
-            // the segment's state: the sum of its chunks, and for the first segment what is left of S0
-            ok = wait.warp(&bar_state, 0) && wait.warp(&bar_upd[(chunks - 1) % ST], (uint32_t)((chunks - 1) / ST) & 1);
-            tc_fence_after_sync();
-            const float decay = ex2(seg_total_s[half]);
-#pragma unroll 1
-            for (int n0 = 0; n0 < N && ok; n0 += 32) {
-                float v[32], start[32];
-                tmem_read32(tbase + TM_S + lanes + n0, v);
-                load_start(n0, start);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = fmaf(decay, start[i], v[i]);
-                store_state(seg_state(unit), n0, v);
-            }
-        } else if (ok && chunks > 0 && last_seg && p.ST && wait.warp(&bar_upd[0], (chunks - 1) & 1)) {
-            // the state after the last token
-            tc_fence_after_sync();
-#pragma unroll 1
-            for (int n0 = 0; n0 < N; n0 += 32) {
-                float v[32];
-                tmem_read32(tbase + TM_S + lanes + n0, v);
-                store_state(p.ST + s_off, n0, v);
-            }
-        }
-    } else if (warp < (STATE_ONLY ? kIssueWarp : kFirstScore)) {
-        // ------------------------------------------------------------ decays and weighted x
-        // one group of four warps; in the state-only kernel three, each every third chunk
-        const int dw = (warp - kFirstDecay) & 3, group = (warp - kFirstDecay) >> 2;
-        constexpr int kGroups = STATE_ONLY ? ST : 1;
-        const int j = 32 * dw + lane;                                    // a token here
-        float rate[NH], bias[NH], raw[NH], total_all[NH];
-#pragma unroll
-        for (int i = 0; i < NH; ++i) {
-            const int head = i ? h1 : h0;
-            rate[i] = p.A[head] * 1.4426950408889634f;                   // decays in powers of two
-            bias[i] = p.dt_bias ? p.dt_bias[head] : 0.f;
-            total_all[i] = 0.f;
-        }
-        // the state-only kernel goes through its chunks from the last to the first: the decay behind a chunk is then
-        // known when its weights are formed, and the products only add up, with no pass over the state in between
-        auto chunk_at = [&](int c) { return STATE_ONLY ? chunks - 1 - c : c; };
-        auto load_dt = [&](int c) {
-            const int t = chunk_at(c) * kTok + j;
-#pragma unroll
-            for (int i = 0; i < NH; ++i)
-                raw[i] = t < len ? load_elem(p.dt, (start + tok0 + t) * p.lddt + (i ? h1 : h0)) : 0.f;
-        };
-        load_dt(group);
-        bool ok = true;
-        for (int c = group; c < chunks; c += kGroups) {
-            Scalars& sc = scal[STATE_ONLY ? group : c & 1];
-            const int n_valid = min(kTok, len - chunk_at(c) * kTok);
-            float sfx[NH], stp[NH];
-#pragma unroll
-            for (int i = 0; i < NH; ++i) stp[i] = raw[i] + bias[i];
-#pragma unroll 1
-            for (int i = 0; i < NH; ++i) {                               // the heads change places: one copy of the code
-                const float st = j < n_valid ? softplus(stp[0]) : 0.f;
-                const float t0 = stp[NH - 1];
-                stp[NH - 1] = st;
-                if (NH == 2) stp[0] = t0;
-            }
-#pragma unroll
-            for (int i = 0; i < NH; ++i) {
-                const float la = stp[i] * rate[i];
-                float incl = la, rev = la;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const float a = __shfl_up_sync(0xffffffffu, incl, off), b = __shfl_down_sync(0xffffffffu, rev, off);
-                    if (lane >= off) incl += a;
-                    if (lane + off < 32) rev += b;
-                }
-                const float after = __shfl_down_sync(0xffffffffu, rev, 1);
-                sfx[i] = lane == 31 ? 0.f : after;                       // tokens after this one in its block
-                sc.neg[i][j] = -incl;
-                sc.step[i][j] = stp[i];
-                sc.col[i][j] = stp[i] * ex2(sfx[i]);
-                if (lane == 31) sc.total[i][dw] = incl;
-            }
-            if (c + kGroups < chunks) load_dt(c + kGroups);
-            named_bar_sync(1 + 2 * group, 32 * kDecayWarps);
-            if constexpr (STATE_ONLY) {
-                // the decay behind the chunk, handed on from group to group
-                if (c > 0) (void)wait.warp(&bar_behind[group], (uint32_t)((c - 1) / ST) & 1);
-#pragma unroll
-                for (int i = 0; i < NH; ++i) total_all[i] = c > 0 ? behind_s[group][i] : 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < NH; ++i) {
-                float after = 0.f, all = 0.f;
-#pragma unroll
-                for (int b = 3; b >= 0; --b) {
-                    if (b > dw) after += sc.total[i][b];
-                    all += sc.total[i][b];
-                }
-                const float w = stp[i] * ex2(sfx[i] + after + (STATE_ONLY ? total_all[i] : 0.f));
-                const __nv_bfloat16 w1 = __float2bfloat16_rn(w), w2 = __float2bfloat16_rn(w - __bfloat162float(w1));
-                sc.w1[i][j] = __bfloat16_as_ushort(w1);
-                sc.w2[i][j] = __bfloat16_as_ushort(w2);
-                total_all[i] += all;
-            }
-            if constexpr (STATE_ONLY) {
-                const int next = (group + 1) % ST;
-                if (j == 0)
-                    for (int i = 0; i < NH; ++i) behind_s[next][i] = total_all[i];
-                warp_arrive(&bar_behind[next], lane);
-            } else {
-                warp_arrive(&bar_scal[c & 1], lane);
-            }
-            ok = wait.warp(&full[c % ST], (uint32_t)(c / ST) & 1);
-            uint8_t* s = sm + (c % ST) * kStageBytes;
-            if (ok && p.cu_seqlens && j >= n_valid) {
-                // rows of other sequences, or of none: zeros, so that nothing of theirs enters a sum
-                const uint4 zero = make_uint4(0, 0, 0, 0);
-                for (int i = 0; i < 8; ++i) {
-                    for (int a = 0; a < 2; ++a) *reinterpret_cast<uint4*>(s + OFF_X + a * ATOM + j * 128 + i * 16) = zero;
-                    for (int a = 0; a < N / 64; ++a) *reinterpret_cast<uint4*>(s + OFF_B + a * ATOM + j * 128 + i * 16) = zero;
-                }
+                tmem_wait_st();
                 fence_proxy_async_smem();
             }
-            // the operand's place is free
-            if constexpr (STATE_ONLY) ok = ok && (c < ST || wait.warp(&bar_upd[group], (uint32_t)(c / ST - 1) & 1));
-            else ok = ok && (c == 0 || wait.warp(&bar_upd[0], (uint32_t)(c - 1) & 1));
-            // w and the zeros of all tokens; all four warps leave together
-            ok = named_bar_and(2 + 2 * group, 32 * kDecayWarps, ok);
-            if (!ok) break;
-            tc_fence_after_sync();
-            // 32 value columns per warp, 32 tokens a step
-            const int half = NH == 2 ? dw >> 1 : 0;
-            const uint32_t* w1 = reinterpret_cast<const uint32_t*>(sc.w1[half]) + (lane & 3);
-            const uint32_t* w2 = reinterpret_cast<const uint32_t*>(sc.w2[half]) + (lane & 3);
-            const uint32_t xa = smem_u32(s) + OFF_X + (dw >> 1) * ATOM + (lane & 7) * 128 +
-                                (((uint32_t)((dw & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
-#pragma unroll 1
-            for (int q4 = 0; q4 < 4; ++q4) {
-                uint32_t hi[2][8], lo[2][8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int tg = 4 * q4 + k;                           // 8 tokens
-                    uint32_t x[4];
-                    ldmatrix4t(xa + tg * 1024, x);
-                    const uint32_t a = w1[4 * tg], b = w2[4 * tg];
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const uint32_t h = mul_bf16x2(x[m], a);
-                        const uint32_t rest = fma_bf16x2(x[m], a, h ^ 0x80008000u);
-                        hi[m >> 1][2 * k + (m & 1)] = h;
-                        lo[m >> 1][2 * k + (m & 1)] = fma_bf16x2(x[m], b, rest);
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const uint32_t at = tbase + lanes + ((uint32_t)(16 * u) << 16) + 16 * q4 + TM_HI - 128 * group;
-                    tmem_st_16x128(at, hi[u]);
-                    tmem_st_16x128(at + 64, lo[u]);
-                }
-            }
-            tmem_wait_st();
             tc_fence_before_sync();
-            warp_arrive(STATE_ONLY ? &bar_wst[group] : &bar_w, lane);
+            if (!(p.skip_handoff && c == 0)) warp_arrive(&bar_state, lane);
+        };
+        if (chunks > 0) {
+            weigh(0);
+            carry(0);
         }
-        if constexpr (STATE_ONLY) if (group == (chunks - 1) % ST) {
-            if (ok && j == 0) {
-                p.seg_decay[(size_t)unit * H + h0] = seg_total_s[0] = total_all[0];
-                if (NH == 2 && h1 != h0) p.seg_decay[(size_t)unit * H + h1] = total_all[NH - 1];
-                seg_total_s[1] = total_all[NH - 1];
-            }
-            warp_arrive(&bar_state, lane);
-        }
-    } else if (!STATE_ONLY) {
-        // ------------------------------------------------------------ Q (the decayed lower triangle of G), outputs
-        const int which = (warp - kFirstScore) >> 2;     // of Q: 16 columns of each 32; of Y: 64 columns
-        const int r = 32 * quarter + lane;
-        const float skip0 = p.D ? p.D[h0] : 0.f, skip1 = p.D ? p.D[h1] : 0.f;
-        const uint32_t yt = tbase + TM_Y + lanes + 64 * which;
-        bool ok = true;
+#pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             const uint32_t par = c & 1;
             const Scalars& sc = scal[c & 1];
-            ok = wait.warp(&bar_scal[c & 1], (c >> 1) & 1) && wait.warp(&bar_g, par);
+            // Q: the decayed lower triangle of G, columns 8 part .. 8 part + 7 of each block of 32
+            (void)wait.warp(&bar_g, par);
             tc_fence_after_sync();
-            float row = 0.f;                             // 2^{L_r}, of this warp's columns of Y
             {
-                float off[48], diag[16];                 // G: blocks 0 to 2 of 32 columns, and the diagonal's
-                tmem_read3x16(tbase + TM_G + lanes + 16 * which, off, tbase + TM_G + lanes + 32 * quarter + 16 * which, diag);
+                float gv[32];
+                tmem_read4x8(tbase + TM_G + lanes + 8 * part, gv);
                 tc_fence_before_sync();
-                // both warps of these lanes have read G (Q takes its place).  They leave only here, together.
-                ok = named_bar_and(3 + quarter, 64, ok);
-                if (!ok) break;
+                named_bar_sync(4 + quarter, 128);                        // all of these lanes' G is read: Q takes its place
                 tc_fence_after_sync();
-#pragma unroll
-                for (int i = 0; i < NH; ++i) {
-                    const uint32_t qt = tbase + TM_G + 64 * i + lanes + 8 * which;
-                    const float* colf = sc.col[i] + 16 * which;
-                    const float lr = -sc.neg[i][r];
-                    float e = lr;                        // sum over the tokens after block b up to r
-#pragma unroll
-                    for (int b = 2; b >= 0; --b) {
-                        if (b >= quarter) continue;
-                        const float ee = ex2(e);
-                        const uint64_t e2 = pair2(ee, ee);
-                        e += sc.total[i][b];
-                        uint32_t q[8];
-#pragma unroll
-                        for (int k = 0; k < 16; k += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(colf + 32 * b + k);
-                            const float* gb = off + 16 * b + k;
-                            q[k / 2] = mul2_bf16x2(pair2(gb[0], gb[1]), mul2(e2, pair2(f.x, f.y)));
-                            q[k / 2 + 1] = mul2_bf16x2(pair2(gb[2], gb[3]), mul2(e2, pair2(f.z, f.w)));
-                        }
-                        tmem_st8(qt + 16 * b, q);
-                    }
-                    if (NH == 1 || i == which) row = ex2(e);
-                    uint32_t q[8];
-                    const float skip = i ? skip1 : skip0;
-                    const float* negd = sc.neg[i] + 32 * quarter + 16 * which;
-                    const float* stepd = sc.step[i] + 32 * quarter + 16 * which;
-                    const int dr = lane - 16 * which;    // the column of the diagonal element
-#pragma unroll
-                    for (int k = 0; k < 16; k += 4) {
-                        const float4 l = *reinterpret_cast<const float4*>(negd + k);
-                        const float4 st = *reinterpret_cast<const float4*>(stepd + k);
-                        const float lj[4] = {l.x, l.y, l.z, l.w}, sj[4] = {st.x, st.y, st.z, st.w};
-                        float v[4];
-#pragma unroll
-                        for (int d = 0; d < 4; ++d) {
-                            const float m = diag[k + d] * (ex2(lr + lj[d]) * sj[d]);
-                            v[d] = k + d < dr ? m : k + d == dr ? m + skip : 0.f;
-                        }
-                        q[k / 2] = bf16x2(v[0], v[1]);
-                        q[k / 2 + 1] = bf16x2(v[2], v[3]);
-                    }
-                    tmem_st8(qt + 16 * quarter, q);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) q[k] = 0u;
 #pragma unroll 1
-                    for (int b = quarter + 1; b < 4; ++b) tmem_st8(qt + 16 * b, q);
+                for (int i = 0; i < NH; ++i) {
+                    const uint32_t qt = tbase + TM_G + 64 * i + lanes + 4 * part;
+                    const float lr = -sc.neg[i][r];
+                    float e = lr;                                        // sum over the tokens after block b up to r
+#pragma unroll
+                    for (int b = 3; b >= 0; --b) {
+                        const float* gb = gv + 8 * b;
+                        const int j0 = 32 * b + 8 * part;
+                        uint32_t q[4] = {0u, 0u, 0u, 0u};
+                        if (b < quarter) {
+                            const float ee = ex2(e);
+                            const uint64_t e2 = pair2(ee, ee);
+                            e += sc.total[i][b];
+#pragma unroll
+                            for (int k = 0; k < 8; k += 4) {
+                                const float4 f = *reinterpret_cast<const float4*>(&sc.col[i][j0 + k]);
+                                q[k / 2] = mul2_bf16x2(pair2(gb[k], gb[k + 1]), mul2(e2, pair2(f.x, f.y)));
+                                q[k / 2 + 1] = mul2_bf16x2(pair2(gb[k + 2], gb[k + 3]), mul2(e2, pair2(f.z, f.w)));
+                            }
+                        } else if (b == quarter) {
+                            const float skip = i ? skip1 : skip0;
+                            const int dr = lane - 8 * part;              // the column of the diagonal element
+#pragma unroll
+                            for (int k = 0; k < 8; k += 4) {
+                                const float4 l = *reinterpret_cast<const float4*>(&sc.neg[i][j0 + k]);
+                                const float4 st = *reinterpret_cast<const float4*>(&sc.step[i][j0 + k]);
+                                const float lj[4] = {l.x, l.y, l.z, l.w}, sj[4] = {st.x, st.y, st.z, st.w};
+                                float v[4];
+#pragma unroll
+                                for (int d = 0; d < 4; ++d) {
+                                    const float m = gb[k + d] * (ex2(lr + lj[d]) * sj[d]);
+                                    v[d] = k + d < dr ? m : k + d == dr ? m + skip : 0.f;
+                                }
+                                q[k / 2] = bf16x2(v[0], v[1]);
+                                q[k / 2 + 1] = bf16x2(v[2], v[3]);
+                            }
+                        }
+                        tmem_st4(qt + 16 * b, q);
+                    }
                 }
             }
-            // Y = C S: row r by 2^{L_r}
-            ok = wait.warp(&bar_cs, par);
-            tc_fence_after_sync();
+            // Y = C S: row r by 2^{L_r}, 32 columns to a part
+            const uint32_t yt = tbase + TM_Y + lanes + 32 * part;
             {
-                float v[64];
-                tmem_read64(yt, v);
-                scale_by<64>(v, row);
+                float sum = -sc.neg[yhead][r];
+                for (int b = 0; b < quarter; ++b) sum += sc.total[yhead][b];
+                const float row = ex2(sum);
+                (void)wait.warp(&bar_cs, par);
+                tc_fence_after_sync();
+                float v[32];
+                tmem_read32(yt, v);
+                scale_by<32>(v, row);
                 tmem_write32(yt, v);
-                tmem_write32(yt + 32, v + 32);
             }
             tmem_wait_st();
             tc_fence_before_sync();
             warp_arrive(&bar_q, lane);
-            // Y, finished: into the chunk's own x tile (all its readers are done), from where the load warp stores it
-            // in whole lines
-            ok = ok && wait.warp(&bar_px, par);
+            warp_arrive(&scal_free[c & 1], lane);                        // the chunk's decays are used up
+
+            // while Q X runs: the next chunk's weighted x and carried state
+            if (c + 1 < chunks) {
+                (void)wait.warp(&bar_upd, par);                          // the operand's place is free
+                weigh(c + 1);
+                carry(c + 1);
+            }
+            // Y, finished: into the chunk's own x tile (all its readers are done), from where it is stored in whole lines
+            const bool ok = wait.warp(&bar_px, par);
             tc_fence_after_sync();
-            uint8_t* tile_y = sm + (c % kStages) * kStageBytes + OFF_X + which * ATOM;
-            const bool whole = !p.cu_seqlens || len - c * kTok >= kTok;
-            const int t = c * kTok + r;
-            __nv_bfloat16* yr = p.y + ((start + tok0 + t) * H + h0) * P + 64 * which;    // heads h0, h0 + 1 are neighbours
-            const bool mine = !(NH == 2 && which == 1 && h1 == h0);
             {
-                float v[64];
-                tmem_read64(yt, v);
-                tc_fence_before_sync();                  // the next C S overwrites Y
+                float v[32];
+                tmem_read32(yt, v);
+                tc_fence_before_sync();                                  // the next C S overwrites Y
                 warp_arrive(&bar_yfree, lane);
+                const bool whole = !p.cu_seqlens || job.len - c * kTok >= kTok;
+                uint8_t* tile = sm + OFF_X + (c % kStages) * kTile;
+                const int t = c * kTok + r;
+                // heads h0 and h0 + 1 are neighbours in y; a head carried twice is stored once
+                const bool mine = ok && t < job.len && !(NH == 2 && part >= 2 && job.h1 == job.h0);
+                __nv_bfloat16* yr = p.y + ((job.start + t) * p.H + job.h0) * P + 32 * part;
 #pragma unroll
-                for (int i = 0; i < 64; i += 8) {
-                    const uint4 o = make_uint4(bf16x2(v[i], v[i + 1]), bf16x2(v[i + 2], v[i + 3]),
-                                               bf16x2(v[i + 4], v[i + 5]), bf16x2(v[i + 6], v[i + 7]));
-                    if (whole) *reinterpret_cast<uint4*>(tile_y + sw128_offset(r, i, ATOM)) = o;
-                    else if (mine && ok && t < len) *reinterpret_cast<uint4*>(yr + i) = o;   // rows past a packed sequence stay
+                for (int i = 0; i < 32; i += 8) {
+                    const uint4 o = make_uint4(bf16x2(v[i], v[i + 1]), bf16x2(v[i + 2], v[i + 3]), bf16x2(v[i + 4], v[i + 5]),
+                                               bf16x2(v[i + 6], v[i + 7]));
+                    if (whole) *reinterpret_cast<uint4*>(tile + sw128_offset(r, 32 * part + i, ATOM)) = o;
+                    else if (mine) *reinterpret_cast<uint4*>(yr + i) = o;        // rows past a packed sequence stay
                 }
             }
             fence_proxy_async_smem();
             warp_arrive(&bar_staged, lane);
+        }
+        // the state after the sequence's last token
+        if (chunks > 0 && job.last && p.ST && wait.warp(&bar_upd, (uint32_t)(chunks - 1) & 1) && has_rows && !abort_s) {
+            tc_fence_after_sync();
+            float v[32];
+            tmem_read32(tbase + TM_S + lanes + 32 * part, v);
+            col.store(p.ST + col.s_off, 32 * part, v);
         }
     }
     tc_fence_before_sync();
@@ -942,36 +1055,41 @@ size_t workspace_of(long long units, int H, int N, int P) {
     return (size_t)units * H * ((size_t)N * P + 1) * sizeof(float);
 }
 
-template <int N, int P, bool STATE_ONLY>
-cudaError_t launch_one(const CUtensorMap& mx, const CUtensorMap& mb, const CUtensorMap& mc, const CUtensorMap& my,
-                       const Params& p, long long units, cudaStream_t s) {
-    static std::mutex mu;
-    static bool attr_set[64] = {false};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    {
+// Shared memory above the default limit, asked for once per kernel and device.
+template <int N, int P, bool STATE>
+struct AllowSmem {
+    static cudaError_t once() {
+        static std::mutex mu;
+        static bool set[64] = {false};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
         std::lock_guard<std::mutex> lock(mu);
-        if (dev >= 64 || !attr_set[dev]) {
-            e = cudaFuncSetAttribute(kda_ssm_tc_kernel<N, P, STATE_ONLY>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_DYN);
-            if (e != cudaSuccess) return e;
-            if (dev < 64) attr_set[dev] = true;
-        }
+        if (dev < 64 && set[dev]) return cudaSuccess;
+        constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        if constexpr (STATE) e = cudaFuncSetAttribute(kda_ssm_state_kernel<N, P>, attr, SMEM_DYN);
+        else e = cudaFuncSetAttribute(kda_ssm_tc_kernel<N, P>, attr, SMEM_DYN);
+        if (e == cudaSuccess && dev < 64) set[dev] = true;
+        return e;
     }
-    const long long grid = units * p.tiles;
-    if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    kda_ssm_tc_kernel<N, P, STATE_ONLY><<<(unsigned)grid, kThreads, SMEM_DYN, s>>>(mx, mb, mc, my, p);
-    return cudaGetLastError();
-}
+};
 
 template <int N, int P>
 cudaError_t launch_np(const CUtensorMap& mx, const CUtensorMap& mb, const CUtensorMap& mc, const CUtensorMap& my,
                       const Params& p, long long units, cudaStream_t s) {
+    const long long grid = units * p.tiles;
+    if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     if (p.seg_chunks > 0) {
-        const cudaError_t e = launch_one<N, P, true>(mx, mb, mc, my, p, units, s);
+        const cudaError_t e = AllowSmem<N, P, true>::once();
         if (e != cudaSuccess) return e;
+        kda_ssm_state_kernel<N, P><<<(unsigned)grid, kStateThreads, SMEM_DYN, s>>>(mx, mb, p);
+        const cudaError_t err = cudaGetLastError();
+        if (err != cudaSuccess) return err;
     }
-    return launch_one<N, P, false>(mx, mb, mc, my, p, units, s);
+    const cudaError_t e = AllowSmem<N, P, false>::once();
+    if (e != cudaSuccess) return e;
+    kda_ssm_tc_kernel<N, P><<<(unsigned)grid, kThreads, SMEM_DYN, s>>>(mx, mb, mc, my, p);
+    return cudaGetLastError();
 }
 
 }  // namespace
