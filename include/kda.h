@@ -399,7 +399,7 @@ typedef enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 } kda_activation;
  *   W         : 2, 3 or 4.  C: a positive multiple of 8.
  *
  * T == 0 copies state to state_out.  Returns KDA_OK; KDA_ERR_UNSUPPORTED for another W, a C that is
- * not a multiple of 8, another dtype or activation.
+ * not a multiple of 8, another dtype or activation; KDA_ERR_INVALID_ARG for a B or T above 2e9 too.
  */
 KDA_API int kda_short_conv(const void* x, const void* weight, const void* bias, const void* state, void* y,
                            void* state_out, int B, int T, int C, int W, long long ldx, long long ldy,

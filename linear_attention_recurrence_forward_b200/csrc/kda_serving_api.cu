@@ -15,6 +15,7 @@ bool head_dim_ok(int d) { return d == 64 || d == 128; }
 
 constexpr double kMostElements = 9.0e15;     // element counts stay far from overflow
 constexpr long long kMostStride = 1ll << 40;
+constexpr int kMostTokens = 2000000000;       // token and sequence counts: sums with a strip stay within 32 bits
 
 struct Range {
     uintptr_t lo, hi;   // [lo, hi)
@@ -35,6 +36,7 @@ bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 int check_conv(const kda::ConvArgs& a, size_t tokens, size_t n_state) {
     if (!dtype_ok(a.dtype) || (a.act != KDA_ACT_NONE && a.act != KDA_ACT_SILU)) return KDA_ERR_UNSUPPORTED;
     if (a.C <= 0 || a.n_seq <= 0 || a.T < 0) return KDA_ERR_INVALID_ARG;
+    if (a.T > kMostTokens || a.n_seq > kMostTokens) return KDA_ERR_INVALID_ARG;
     if (a.W < 2 || a.W > 4 || a.C % 8 != 0) return KDA_ERR_UNSUPPORTED;
     const size_t es = elem_size(a.dtype);
     const long long vec = (long long)(16 / es);
@@ -267,7 +269,7 @@ int kda_ssm_forward(const void* x, const void* dt, const float* A, const void* B
                     const float* dt_bias, const float* S0, void* y, float* S_T, int B, int T, int H, int G, int N,
                     int P, long long ldx, long long lddt, long long ldb, long long ldc, int dtype, int impl,
                     void* workspace, size_t workspace_bytes, struct CUstream_st* stream) {
-    if (B <= 0 || T < 0 || (double)B * T > 2.0e9) return KDA_ERR_INVALID_ARG;
+    if (B <= 0 || T < 0 || (double)B * T > kMostTokens) return KDA_ERR_INVALID_ARG;
     kda::SsmArgs a{x, dt, A, Bm, Cm, D, dt_bias, S0, y, S_T, nullptr, B, T, H, G, N, P, ldx, lddt, ldb, ldc, dtype,
                    nullptr, 0, nullptr, kda::wait_timeout_ns(), workspace, kda::wait_fault_mode()};
     return run_ssm(a, (size_t)B * T, impl, workspace_bytes, stream);
@@ -278,7 +280,7 @@ int kda_ssm_forward_varlen(const void* x, const void* dt, const float* A, const 
                            float* S_T, int n_seq, int T_total, int H, int G, int N, int P, long long ldx,
                            long long lddt, long long ldb, long long ldc, int dtype, int impl, void* workspace,
                            size_t workspace_bytes, struct CUstream_st* stream) {
-    if (n_seq <= 0 || T_total < 0 || T_total > 2000000000 || !cu_seqlens) return KDA_ERR_INVALID_ARG;
+    if (n_seq <= 0 || T_total < 0 || T_total > kMostTokens || !cu_seqlens) return KDA_ERR_INVALID_ARG;
     kda::SsmArgs a{x, dt, A, Bm, Cm, D, dt_bias, S0, y, S_T, cu_seqlens, n_seq, T_total, H, G, N, P, ldx, lddt, ldb,
                    ldc, dtype, nullptr, 0, nullptr, kda::wait_timeout_ns(), workspace, kda::wait_fault_mode()};
     return run_ssm(a, (size_t)T_total, impl, workspace_bytes, stream);

@@ -76,6 +76,15 @@ def test_refusals(L, form):
         assert f(cu=BASE + 3 * SZ) == INVALID              # the slot table inside the pool
 
 
+@pytest.mark.parametrize("form", ["batch", "varlen", "step", "paged"])
+def test_counts_near_32_bits_are_refused(L, form):
+    """More than 2e9 tokens of a sequence, or sequences: sums with a strip or a group would pass 32 bits."""
+    far = {k: BASE + i * (1 << 42) for i, k in enumerate(ptrs())}
+    assert call(L, form, B=2 ** 31 - 2, T=0, C=8, **far) == INVALID
+    if form in ("batch", "varlen"):
+        assert call(L, form, B=1, T=2 ** 31 - 2, C=8, **far) == INVALID
+
+
 def test_binding_refuses_bad_tensors():
     x, w = torch.zeros(2, 5, 64), torch.zeros(64, 4)
     with pytest.raises(ValueError):
