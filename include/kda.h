@@ -460,8 +460,8 @@ KDA_API int kda_short_conv_step_paged(const void* x, const void* weight, const v
  *   workspace, workspace_bytes : DEVICE memory of at least kda_ssm_workspace(...) bytes, 16-byte
  *             aligned (NULL when that is 0), not used by anything else until the work is done.
  *
- * The tensor-core kernel forms whole 128-token blocks: a non-finite value in one token's x or B may
- * reach the outputs of other tokens of its block, earlier ones too.  T == 0 copies S0 to S_T.
+ * The tensor-core kernel forms whole 128-token blocks: a non-finite value in one token's x, B or dt
+ * may reach the outputs of other tokens of its block, earlier ones too.  T == 0 copies S0 to S_T.
  */
 KDA_API int kda_ssm_forward(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
                             const float* D, const float* dt_bias, const float* S0, void* y, float* S_T, int B,

@@ -61,6 +61,9 @@ using namespace sm100;
 
 constexpr int kTok = 128;                    // tokens per chunk
 constexpr int kCols = 128;                   // value columns per CTA
+// A token's decay (log 2) is not taken below this: every exponential over such a token is zero all the same, and the
+// sums before and after it differ by few enough that the differences of later ones keep their digits.
+constexpr float kLeastDecay = -160.f;
 constexpr int kStages = 3;                   // of x, which is y's place when it is done
 constexpr int kStateStages = 3;              // of B and x together, in the state-only kernel
 constexpr int kWorkers = 16;                 // warps that do the arithmetic
@@ -799,7 +802,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             for (int k = 0; k < 4; ++k) {
                 step[k] = c * kTok + 32 * k + lane < job.len
                               ? softplus(__bfloat162float(__ushort_as_bfloat16(raw[k])) + bias) : 0.f;
-                block_sums(step[k] * rate, lane, incl[k], after[k]);
+                block_sums(fmaxf(step[k] * rate, kLeastDecay), lane, incl[k], after[k]);
                 total[k] = __shfl_sync(0xffffffffu, incl[k], 31);
             }
             load_dt(n + 2);

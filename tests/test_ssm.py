@@ -150,6 +150,18 @@ def test_strong_and_weak_decay(dtype, impl, step, rate):
 
 @gpu
 @pytest.mark.parametrize("dtype,impl", IMPLS)
+@pytest.mark.parametrize("T,H", [(260, 3), (1700, 1)])
+def test_tokens_that_forget_everything(dtype, impl, T, H):
+    """Time steps of a million here and there: the decay between the tokens after one does not come out of the
+    difference of two sums of millions."""
+    c = case((1, T), H, 1, 128, 64, dtype, seed=5)
+    c["dt"][0, 3::37] = 1e6
+    y, S = kda.kda_ssm_forward(**c, impl=impl)
+    check(y[0], S[0], c, 0, 0, dtype, impl)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,impl", IMPLS)
 def test_optional_arguments_and_state_in_place(dtype, impl):
     c = case((2, 140), 4, 2, 128, 64, dtype, seed=5)
     y, S = kda.kda_ssm_forward(c["x"], c["dt"], c["A"], c["Bm"], c["Cm"], impl=impl)      # no D, no bias, S0 = 0
