@@ -286,6 +286,9 @@ kda_short_conv_kernel(const T* __restrict__ x, const T* __restrict__ weight, con
     }
 }
 
+// The step: each sequence's state is read, shifted and written back whole.  One B200, 256 sequences x 36864
+// channels, bf16, states in a pool: 29 us for 151 MB, 0.80 of the measured copy rate (the first and last
+// microseconds, when loads or stores alone are under way, are a good part of so short a launch).
 constexpr int kStepSeqs = 2;    // sequences in flight per thread of the step kernel
 
 template <typename T, int W>
