@@ -275,6 +275,12 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
     if (lane == 0) mbar_arrive(bar);
 }
 
+// The second launch of a call may start while the first one runs: the first lets it once all of its CTAs are on their
+// SMs; the second sets itself up, starts its loads, and waits for the first one's end (and its writes).  4096 tokens,
+// 32 heads of 128: 55.5 us, one after the other 59.
+__device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The tokens and heads of a CTA.
 struct Job {
     int unit, unit0, seq, seg, n_seg;        // unit: the sequence's segment; unit0: its first segment
@@ -491,6 +497,7 @@ kda_ssm_state_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     __shared__ volatile int abort_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3;
     Job job;
+    let_next_launch_start();
     if (!find_job<NH>(p, job) || job.last) return;
     const int chunks = job.chunks;           // all whole
     if (tid == 0) {
@@ -721,6 +728,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 return true;
             };
             for (int c = 0; c < kStages - 1; ++c) x_in(c);
+            wait_for_launch_before();
             bool ok = true;
             for (int c = 0; c < chunks; ++c) {
                 // B and C are used up once the chunk before has updated the state (and all products before that have run)
@@ -752,6 +760,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             const uint32_t id_cs = idesc_bf16_f32(128, kCols, false, false);
             const uint32_t id_px = idesc_bf16_f32(128, P, false, true);
             const uint32_t id_up = idesc_bf16_f32(128, N, false, true);
+            wait_for_launch_before();
             for (int c = 0; c < chunks; ++c) {
                 const uint32_t par = c & 1;
                 // products run in order: G takes the place that Q X of the chunk before has read
@@ -794,6 +803,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             }
         };
         load_dt(warp - kDecayWarp);
+        wait_for_launch_before();
         for (int n = warp - kDecayWarp; n < chunks * NH; n += 2) {
             const int c = n / NH, i = n % NH;
             const float rate = i ? rate1 : rate0, bias = i ? bias1 : bias0;
@@ -833,6 +843,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         const int yhead = NH == 2 ? part >> 1 : 0;                       // head of this warp's columns of Y
         const Column<N, P> col(p, job, r);
         const bool has_rows = 32 * part < N;                             // of S: 32 rows to a part
+        wait_for_launch_before();
         if (has_rows) {
             float v[32];
             col.load_start(32 * part, v);
@@ -1091,8 +1102,17 @@ cudaError_t launch_np(const CUtensorMap& mx, const CUtensorMap& mb, const CUtens
     }
     const cudaError_t e = AllowSmem<N, P, false>::once();
     if (e != cudaSuccess) return e;
-    kda_ssm_tc_kernel<N, P><<<(unsigned)grid, kThreads, SMEM_DYN, s>>>(mx, mb, mc, my, p);
-    return cudaGetLastError();
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = SMEM_DYN;
+    cfg.stream = s;
+    cfg.attrs = &early;
+    cfg.numAttrs = p.seg_chunks > 0 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kda_ssm_tc_kernel<N, P>, mx, mb, mc, my, p);
 }
 
 }  // namespace

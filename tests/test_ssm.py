@@ -330,6 +330,29 @@ def test_segments(B, T, H, G, N, P):
 
 
 @gpu
+def test_segments_in_graphs_and_beside_another_stream():
+    """Both launches of a call captured and replayed, twice over in one graph, while another stream runs a call of
+    its own: the second launch may start early, and must not read what the first has not written."""
+    c = [case((1, 4096), 4, 1, 128, 128, "bf16", seed=s, rate=1.5) for s in (1, 2, 3)]
+    want = [kda.kda_ssm_forward(**k) for k in c]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [kda.kda_ssm_forward(**k) for k in c[:2]]
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        for y, S in got:
+            y.zero_()
+            S.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        y3, S3 = kda.kda_ssm_forward(**c[2], stream=side)
+        torch.cuda.synchronize()
+        for (y, S), (yw, Sw) in zip(got + [(y3, S3)], want):
+            assert torch.equal(y, yw) and torch.equal(S, Sw)
+    assert kda.kda_get_device_status() == 0
+
+
+@gpu
 def test_segments_packed():
     lengths, lead, tail = [3000, 0, 129, 2500, 1500], 3, 5
     T, H, G, N, P = lead + sum(lengths) + tail, 2, 1, 128, 64
