@@ -22,7 +22,9 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -531,7 +533,7 @@ def _on_device(dev: torch.device):
     """The device of the tensors made current for a call (nothing to do when it is already)."""
     if dev.type != "cuda":
         raise ValueError(f"expected CUDA tensors, got {dev}")
-    if dev.index == torch.cuda.current_device():
+    if dev.index == torch._C._cuda_getDevice():
         return _SAME_DEVICE
     return torch.cuda.device(dev)
 
@@ -553,9 +555,19 @@ def _empty(shape, dtype, dev, stream, like=None) -> torch.Tensor:
     return torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _dense(t, name: str, shape: tuple, dtype, device) -> None:
+    """_check, in one expression when all is well (these checks are a good part of a small call's host time)."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.device == device
+            and t.is_contiguous()):
+        _check(t, name, shape, dtype, device)
+
+
 def _rows(t, name: str, lead, row, dtype, device) -> int:
     """Check a tensor of shape lead + row whose rows are contiguous and evenly spaced (a slice of wider rows
     is fine); returns the spacing in elements."""
+    if isinstance(t, torch.Tensor) and t.is_contiguous() and t.shape == lead + row and t.dtype == dtype \
+            and t.device == device:
+        return math.prod(row)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -586,7 +598,7 @@ def _rows(t, name: str, lead, row, dtype, device) -> int:
 
 def _vector(t, name: str, n: int, dtype, device):
     if t is not None:
-        _check(t, name, (n,), dtype, device)
+        _dense(t, name, (n,), dtype, device)
     return _ptr(t)
 
 
@@ -603,7 +615,7 @@ def _conv_common(x, lead, weight, bias, y, activation, stream):
     _dtype_code(dt)
     if activation not in ACTIVATION:
         raise ValueError(f"unknown activation {activation!r}")
-    _check(weight, "weight", (C, W), dt, dev)
+    _dense(weight, "weight", (C, W), dt, dev)
     b = _vector(bias, "bias", C, dt, dev)
     ldx = _rows(x, "x", lead, (C,), dt, dev)
     if y is None:
@@ -622,9 +634,9 @@ def kda_short_conv(x, weight, bias=None, state=None, *, activation="silu", y=Non
     C, W, y, ldx, ldy, w, b, act = _conv_common(x, (B, T), weight, bias, y, activation, stream)
     dev, dt = x.device, x.dtype
     if state is not None:
-        _check(state, "state", (B, W - 1, C), dt, dev)
+        _dense(state, "state", (B, W - 1, C), dt, dev)
     if state_out is not None:
-        _check(state_out, "state_out", (B, W - 1, C), dt, dev)
+        _dense(state_out, "state_out", (B, W - 1, C), dt, dev)
     elif return_state:
         state_out = _empty((B, W - 1, C), dt, dev, stream, state)
     with _on_device(dev):
@@ -643,11 +655,11 @@ def kda_short_conv_varlen(x, weight, cu_seqlens, bias=None, state=None, *, activ
     N = cu_seqlens.shape[0] - 1
     C, W, y, ldx, ldy, w, b, act = _conv_common(x, (T_total,), weight, bias, y, activation, stream)
     dev, dt = x.device, x.dtype
-    _check(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
+    _dense(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
     if state is not None:
-        _check(state, "state", (N, W - 1, C), dt, dev)
+        _dense(state, "state", (N, W - 1, C), dt, dev)
     if state_out is not None:
-        _check(state_out, "state_out", (N, W - 1, C), dt, dev)
+        _dense(state_out, "state_out", (N, W - 1, C), dt, dev)
     elif return_state:
         state_out = _empty((N, W - 1, C), dt, dev, stream, state)
     with _on_device(dev):
@@ -664,7 +676,7 @@ def kda_short_conv_step(x, weight, state, bias=None, *, activation="silu", y=Non
     B = x.shape[0]
     C, W, y, ldx, ldy, w, b, act = _conv_common(x, (B,), weight, bias, y, activation, stream)
     dev, dt = x.device, x.dtype
-    _check(state, "state", (B, W - 1, C), dt, dev)
+    _dense(state, "state", (B, W - 1, C), dt, dev)
     with _on_device(dev):
         rc = lib().kda_short_conv_step(x.data_ptr(), w, b, state.data_ptr(), y.data_ptr(), B, C, W, ldx, ldy, act,
                                        DTYPE[dt], _stream_on(dev, stream))
@@ -680,8 +692,8 @@ def kda_short_conv_step_paged(x, weight, state_pool, slots, bias=None, *, activa
     C, W, y, ldx, ldy, w, b, act = _conv_common(x, (B,), weight, bias, y, activation, stream)
     dev, dt = x.device, x.dtype
     n_slots = state_pool.shape[0]
-    _check(state_pool, "state_pool", (n_slots, W - 1, C), dt, dev)
-    _check(slots, "slots", (B,), torch.int32, dev)
+    _dense(state_pool, "state_pool", (n_slots, W - 1, C), dt, dev)
+    _dense(slots, "slots", (B,), torch.int32, dev)
     with _on_device(dev):
         rc = lib().kda_short_conv_step_paged(x.data_ptr(), w, b, state_pool.data_ptr(), n_slots, slots.data_ptr(),
                                              y.data_ptr(), B, C, W, ldx, ldy, act, DTYPE[dt], _stream_on(dev, stream))
@@ -698,12 +710,12 @@ def _ssm_common(x, dt, A, Bm, Cm, D, dt_bias, lead, y, stream):
     _dtype_code(ty)
     lds = (_rows(x, "x", lead, (H, P), ty, dev), _rows(dt, "dt", lead, (H,), ty, dev),
            _rows(Bm, "Bm", lead, (G, N), ty, dev), _rows(Cm, "Cm", lead, (G, N), ty, dev))
-    _check(A, "A", (H,), torch.float32, dev)
+    _dense(A, "A", (H,), torch.float32, dev)
     d, bias = _vector(D, "D", H, torch.float32, dev), _vector(dt_bias, "dt_bias", H, torch.float32, dev)
     if y is None:
         y = _empty(lead + (H, P), ty, dev, stream, x)
     else:
-        _check(y, "y", lead + (H, P), ty, dev)
+        _dense(y, "y", lead + (H, P), ty, dev)
     return H, G, N, P, y, lds, d, bias
 
 
@@ -736,9 +748,9 @@ def kda_ssm_forward(x, dt, A, Bm, Cm, D=None, dt_bias=None, S0=None, *, y=None, 
     H, G, N, P, y, lds, d, bias = _ssm_common(x, dt, A, Bm, Cm, D, dt_bias, (B, T), y, stream)
     dev, ty = x.device, x.dtype
     if S0 is not None:
-        _check(S0, "S0", (B, H, N, P), torch.float32, dev)
+        _dense(S0, "S0", (B, H, N, P), torch.float32, dev)
     if S_T is not None:
-        _check(S_T, "S_T", (B, H, N, P), torch.float32, dev)
+        _dense(S_T, "S_T", (B, H, N, P), torch.float32, dev)
     elif return_state:
         S_T = _empty((B, H, N, P), torch.float32, dev, stream, S0)
     with _on_device(dev):
@@ -760,11 +772,11 @@ def kda_ssm_forward_varlen(x, dt, A, Bm, Cm, cu_seqlens, D=None, dt_bias=None, S
     n_seq = cu_seqlens.shape[0] - 1
     H, G, N, P, y, lds, d, bias = _ssm_common(x, dt, A, Bm, Cm, D, dt_bias, (T_total,), y, stream)
     dev, ty = x.device, x.dtype
-    _check(cu_seqlens, "cu_seqlens", (n_seq + 1,), torch.int32, dev)
+    _dense(cu_seqlens, "cu_seqlens", (n_seq + 1,), torch.int32, dev)
     if S0 is not None:
-        _check(S0, "S0", (n_seq, H, N, P), torch.float32, dev)
+        _dense(S0, "S0", (n_seq, H, N, P), torch.float32, dev)
     if S_T is not None:
-        _check(S_T, "S_T", (n_seq, H, N, P), torch.float32, dev)
+        _dense(S_T, "S_T", (n_seq, H, N, P), torch.float32, dev)
     elif return_state:
         S_T = _empty((n_seq, H, N, P), torch.float32, dev, stream, S0)
     with _on_device(dev):
@@ -784,7 +796,7 @@ def kda_ssm_decode_step(x, dt, A, Bm, Cm, S, D=None, dt_bias=None, *, y=None, st
     B = x.shape[0]
     H, G, N, P, y, lds, d, bias = _ssm_common(x, dt, A, Bm, Cm, D, dt_bias, (B,), y, stream)
     dev, ty = x.device, x.dtype
-    _check(S, "S", (B, H, N, P), torch.float32, dev)
+    _dense(S, "S", (B, H, N, P), torch.float32, dev)
     with _on_device(dev):
         rc = lib().kda_ssm_decode_step(x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), d,
                                        bias, S.data_ptr(), y.data_ptr(), B, H, G, N, P, *lds, DTYPE[ty],
@@ -801,8 +813,8 @@ def kda_ssm_decode_step_paged(x, dt, A, Bm, Cm, S_pool, slots, D=None, dt_bias=N
     H, G, N, P, y, lds, d, bias = _ssm_common(x, dt, A, Bm, Cm, D, dt_bias, (B,), y, stream)
     dev, ty = x.device, x.dtype
     n_slots = S_pool.shape[0]
-    _check(S_pool, "S_pool", (n_slots, H, N, P), torch.float32, dev)
-    _check(slots, "slots", (B,), torch.int32, dev)
+    _dense(S_pool, "S_pool", (n_slots, H, N, P), torch.float32, dev)
+    _dense(slots, "slots", (B,), torch.int32, dev)
     with _on_device(dev):
         rc = lib().kda_ssm_decode_step_paged(x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(),
                                              d, bias, S_pool.data_ptr(), n_slots, slots.data_ptr(), y.data_ptr(), B,
@@ -813,7 +825,7 @@ def kda_ssm_decode_step_paged(x, dt, A, Bm, Cm, S_pool, slots, D=None, dt_bias=N
 
 
 def _pools(pools, name: str, device=None, beside=None):
-    """The kda_pool descriptions of a list of pool tensors [n_slots, ...]: (array, number of slots, device).
+    """The kda_pool descriptions of a list of pool tensors [n_slots, ...]: (their bytes, number of slots, device).
 
     Dimension 0 counts the slots.  The others are contiguous, or dimension 1 is spaced wider (the boundary
     states of one batch entry, S_mid[b].transpose(0, 1) of kda_forward_chunked_states).  A pool whose
@@ -846,7 +858,7 @@ def _pools(pools, name: str, device=None, beside=None):
         else:
             raise ValueError(f"{name}: a pool's slots must be contiguous, or contiguous runs along dimension 1")
         flat += (t.data_ptr(), (stride[0] if n_slots > 1 else max(stride[0], run)) * es, pieces, apart * es, run * es)
-    return (ctypes.c_longlong * len(flat))(*flat), n_slots, device
+    return struct.pack(f"{len(flat)}q", *flat), n_slots, device
 
 
 def kda_pool_copy(pools, src, dst, *, src_pools=None, stream=None) -> None:
@@ -866,8 +878,8 @@ def kda_pool_copy(pools, src, dst, *, src_pools=None, stream=None) -> None:
         to, n_dst, dev = _pools(pools, "pools", beside=src_pools)
         frm, n_src, _ = _pools(src_pools, "src_pools", dev, beside=pools)
     n = src.shape[0]
-    _check(src, "src", (n,), torch.int32, dev)
-    _check(dst, "dst", (n,), torch.int32, dev)
+    _dense(src, "src", (n,), torch.int32, dev)
+    _dense(dst, "dst", (n,), torch.int32, dev)
     with _on_device(dev):
         rc = lib().kda_pool_copy(to, frm, len(pools), n_dst, n_src, src.data_ptr(), dst.data_ptr(), n,
                                  _stream_on(dev, stream))
@@ -879,7 +891,7 @@ def kda_pool_clear(pools, slots, *, stream=None) -> None:
     """Set the listed slots (int32 [n] on the device, negative entries skipped) of every pool to zero."""
     to, n_slots, dev = _pools(pools, "pools")
     n = slots.shape[0]
-    _check(slots, "slots", (n,), torch.int32, dev)
+    _dense(slots, "slots", (n,), torch.int32, dev)
     with _on_device(dev):
         rc = lib().kda_pool_clear(to, len(pools), n_slots, slots.data_ptr(), n, _stream_on(dev, stream))
     if rc != 0:
@@ -892,17 +904,17 @@ def kda_pool_compact(pools, slots, done=None, *, out=None, workspace=None, strea
     `slots` itself.  `workspace`: int32 [n_slots + 1] on the device, allocated if not given."""
     to, n_slots, dev = _pools(pools, "pools")
     B = slots.shape[0]
-    _check(slots, "slots", (B,), torch.int32, dev)
+    _dense(slots, "slots", (B,), torch.int32, dev)
     if done is not None:
-        _check(done, "done", (B,), torch.uint8 if done.dtype == torch.uint8 else torch.bool, dev)
+        _dense(done, "done", (B,), torch.uint8 if done.dtype == torch.uint8 else torch.bool, dev)
     if out is None:
         out = _empty((B,), torch.int32, dev, stream, slots)
     else:
-        _check(out, "out", (B,), torch.int32, dev)
+        _dense(out, "out", (B,), torch.int32, dev)
     if workspace is None:
         workspace = _empty((n_slots + 1,), torch.int32, dev, stream)
     else:
-        _check(workspace, "workspace", (n_slots + 1,), torch.int32, dev)
+        _dense(workspace, "workspace", (n_slots + 1,), torch.int32, dev)
     with _on_device(dev):
         rc = lib().kda_pool_compact(to, len(pools), n_slots, slots.data_ptr(), _ptr(done), out.data_ptr(), B,
                                     workspace.data_ptr(), _stream_on(dev, stream))
