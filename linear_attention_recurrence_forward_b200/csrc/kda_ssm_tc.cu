@@ -25,20 +25,22 @@
 // What bounds it.  Per chunk of a 128-column tile HBM moves 64 KB of x and y (2.8K cycles at the measured
 // copy rate with all SMs at it), the tensor core needs 2.5K cycles, and shared memory 3.5K (the products'
 // operands and the tiles' own way in and out).  A chunk takes about 5.5K (4 x 8192 tokens, 96 heads of 128:
-// 590 us, 3.0 TB/s of x and y), and the arithmetic warps are at work in nearly all of them: their chain of steps,
-// each a pass from tensor memory through registers and back, is what bounds it.  So operands are kept out of
-// shared memory where a product allows: Q and the weighted x are tensor-memory operands, and the state is
-// held transposed (lanes = value columns) for that.  The weighted x is transposed on its way by ldmatrix and
-// the 16x128b stores, whose fragments have one layout.
+// 590 us, 2.7 TB/s of x and y; 690 us with a cold L2), 5K where nothing contends.  Loops of about one length
+// bound it: the warps' own steps, each a pass from tensor memory through registers and back; C S, the
+// update, the weighted x and the carried state, which wait for one another; and the loads of B and C.  With
+// any one step's arithmetic taken out a chunk is 2 to 6 % shorter.  Operands are kept out of shared memory
+// where a product allows: Q and the weighted x are tensor-memory operands, and the state is held transposed
+// (lanes = value columns) for that.  The weighted x is transposed on its way by ldmatrix and the 16x128b
+// stores, whose fragments have one layout.
 //
 // Sixteen warps do every step together, a quarter of the columns or tokens to a group of four, in an order
-// that lets the products run behind them: Q while Y = C S runs, the next chunk's weighted x and
-// carried state while Q X runs.  Four more warps issue the products, move the tiles, and form the decays two
-// chunks ahead; the products and the copies follow one another in one thread each.  Warps that keep
-// to one step each, 21 of them, took 10 % longer with two heads to a tile (480 against 424 us at 4 x 8192
-// tokens, 96 heads of 64; 894 against 788 us at 65536) and the same with one.  x has three stages: a tile is y's place when it is done,
-// and is read out (1.8K cycles) while the next two are at work; B and C have one, free once the state is
-// updated.  Tensor memory (512 columns): S^T, Y, G (then Q in its place), weighted x hi and lo.
+// that lets the products run behind them: Q while Y = C S runs, the next chunk's weighted x and carried
+// state while Q X runs.  Four more warps issue the products, move the tiles, and form the decays two chunks
+// ahead; the products and the copies follow one another in one thread each.  Warps that keep to one step
+// each, 21 of them, took 10 % longer with two heads to a tile (480 against 424 us at 4 x 8192 tokens, 96
+// heads of 64; 894 against 788 us at 65536) and the same with one.  x has three stages: a tile is y's place
+// when it is done, and is read out (1.8K cycles) while the next two are at work; B and C have one, free once
+// the state is updated.  Tensor memory (512 columns): S^T, Y, G (then Q in its place), weighted x hi and lo.
 //
 // Long prompts with few heads: the tokens are cut into segments.  A first launch forms the state of every
 // segment but the last (B and x only; the first one from S0, the others from zero), going through the

@@ -4,9 +4,9 @@
 // kPools pools in its parameters, so a model's layers go together (a 2 MB slot is 64 blocks' worth of
 // work: one layer alone would not fill the GPU).  The work is a flat list of (pool, 32 KB part of a
 // slot, pair); a fixed grid of blocks walks it, each part as eight 16-byte loads per thread before the
-// first store.  One B200: compacting 192 slots of 256 in eight layers' scan and convolution pools 353 to 392 us
-// for 2.2 GB (0.87 to 0.96 of the measured copy rate, by which slots move); eight forks of one slot in four layers 17 us, which
-// is as long as the host takes for the call (78 MB: 12 us).
+// first store.  One B200: compacting 192 slots of 256 in eight layers' scan and convolution pools takes
+// 353 to 392 us for 2.2 GB (0.87 to 0.96 of the measured copy rate, by which slots move); eight forks of
+// one slot in four layers 17 us, as long as the host takes for the call (78 MB: 12 us).
 //
 // Pairs are checked where they are used, against the whole list: a pair whose destination another pair
 // has too, or (same pool) another pair reads, is left out and reported, so no two blocks ever write
