@@ -24,23 +24,25 @@
 //
 // What bounds it.  Per chunk of a 128-column tile HBM moves 64 KB of x and y (2.8K cycles at the measured
 // copy rate with all SMs at it), the tensor core needs 2.5K cycles, and shared memory 3.5K (the products'
-// operands and the tiles' own way in and out).  A chunk takes about 5.5K (4 x 8192 tokens, 96 heads of 128:
-// 590 us, 2.7 TB/s of x and y; 690 us with a cold L2), 5K where nothing contends.  Loops of about one length
+// operands and the tiles' own way in and out).  A chunk takes about 4.9K (4 x 8192 tokens, 96 heads of 128:
+// 530 us, 3.0 TB/s of x and y; more with a cold L2), 4.2K where nothing contends.  Loops of about one length
 // bound it: the warps' own steps, each a pass from tensor memory through registers and back; C S, the
-// update, the weighted x and the carried state, which wait for one another; and the loads of B and C.  With
-// any one step's arithmetic taken out a chunk is 2 to 6 % shorter.  Operands are kept out of shared memory
-// where a product allows: Q and the weighted x are tensor-memory operands, and the state is held transposed
-// (lanes = value columns) for that.  The weighted x is transposed on its way by ldmatrix and the 16x128b
-// stores, whose fragments have one layout.
+// update, the weighted x and the carried state, which wait for one another; and the loads of B and C.
+// Operands are kept out of shared memory where a product allows: Q and the weighted x are tensor-memory
+// operands, and the state is held transposed (lanes = value columns) for that.  The weighted x is transposed
+// on its way by ldmatrix and the 16x128b stores, whose fragments have one layout.
 //
 // Sixteen warps do every step together, a quarter of the columns or tokens to a group of four, in an order
 // that lets the products run behind them: Q while Y = C S runs, the next chunk's weighted x and carried
 // state while Q X runs.  Four more warps issue the products, move the tiles, and form the decays two chunks
-// ahead; the products and the copies follow one another in one thread each.  Warps that keep to one step
-// each, 21 of them, took 10 % longer with two heads to a tile (480 against 424 us at 4 x 8192 tokens, 96
-// heads of 64; 894 against 788 us at 65536) and the same with one.  x has three stages: a tile is y's place
-// when it is done, and is read out (1.8K cycles) while the next two are at work; B and C have one, free once
-// the state is updated.  Tensor memory (512 columns): S^T, Y, G (then Q in its place), weighted x hi and lo.
+// ahead.  Warps that keep to one step each, 21 of them, took 10 % longer with two heads to a tile (480 against
+// 424 us at 4 x 8192 tokens, 96 heads of 64) and the same with one.  The issuing and the loading warp run
+// whole, with one elected thread at the products and copies, and the warp's number is made uniform: the
+// compiler then keeps descriptors and addresses in uniform registers (issued by a lane that merely compares
+// itself with 0, each product cost 90 cycles of the thread, more than it takes: 599 against 530 us).
+// x has three stages: a tile is y's place when it is done, and is read out (1.8K cycles) while the next two
+// are at work; B and C have one, free once they are used.  Tensor memory (512 columns): S^T, Y, G (then Q in
+// its place), weighted x hi and lo.
 //
 // Long prompts with few heads: the tokens are cut into segments.  A first launch forms the state of every
 // segment but the last (B and x only; the first one from S0, the others from zero), going through the
@@ -272,6 +274,15 @@ struct Waiter {
     }
 };
 
+// A value that is the same in all lanes, so that the compiler knows it.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+// true in one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
@@ -491,13 +502,13 @@ kda_ssm_state_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_u32(smem_raw);
     uint8_t* sm = smem_raw + (((raw_base + 1023u) & ~1023u) - raw_base);
-    const uint32_t sb = smem_u32(sm);
+    const uint32_t sb = (raw_base + 1023u) & ~1023u;
     __shared__ Scalars scal[ST];
     __shared__ uint64_t full[ST], empty[ST], bar_w[ST], bar_upd[ST], bar_behind[ST], bar_total, bar_drain;
     __shared__ float behind_s[ST][2], total_s[2];
     __shared__ uint32_t tmem_base_s;
     __shared__ volatile int abort_s;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, quarter = warp & 3;
     Job job;
     let_next_launch_start();
     if (!find_job<NH>(p, job) || job.last) return;
@@ -524,42 +535,50 @@ kda_ssm_state_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tbase = tmem_base_s;
+    constexpr uint32_t tbase = 0;            // all columns are this CTA's
     const Waiter wait{&abort_s, p.status, p.timeout_ns};
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     auto row_of = [&](int c) { return job.row0 + (chunks - 1 - c) * kTok; };   // from the last chunk to the first
 
     if (warp == 17) {
-        if (lane == 0) {
-            int issued = 0;
-            for (int c = 0; c < chunks; ++c) {
-                if (c >= ST && !wait.one(&empty[c % ST], (uint32_t)(c / ST - 1) & 1)) break;
+        const bool leader = elect_one();
+        int issued = 0;
+        for (int c = 0; c < chunks; ++c) {
+            if (c >= ST && !wait.warp(&empty[c % ST], (uint32_t)(c / ST - 1) & 1)) break;
+            if (leader) {
                 uint8_t* stage = sm + (c % ST) * kStageBytes;
                 mbar_arrive_expect_tx(&full[c % ST], ATOM * (2 + N / 64));
                 load_bc<N>(stage, &tm_b, &full[c % ST], job, row_of(c));
                 load_x<NH>(stage + kTile, &tm_x, &full[c % ST], job, row_of(c));
-                ++issued;
                 if (c + ST < chunks) prefetch_x<NH>(&tm_x, job, row_of(c + ST));
             }
-            // nothing may be in flight when the CTA exits
-            for (int c = max(0, issued - ST); c < issued; ++c)
-                if (!mbar_wait(&full[c % ST], (uint32_t)(c / ST) & 1, p.timeout_ns)) report_status(p.status, KDA_ERR_TIMEOUT);
+            __syncwarp();
+            ++issued;
         }
+        // nothing may be in flight when the CTA exits
+        for (int c = max(0, issued - ST); c < issued; ++c)
+            if (leader && !mbar_wait(&full[c % ST], (uint32_t)(c / ST) & 1, p.timeout_ns)) report_status(p.status, KDA_ERR_TIMEOUT);
+        __syncwarp();
     } else if (warp == 16) {
-        if (lane == 0) {
-            const uint32_t id_up = idesc_bf16_f32(128, N, false, true);
-            for (int c = 0; c < chunks; ++c) {
-                const uint32_t b_tile = sb + (c % ST) * kStageBytes, w = tbase + TM_W - 128 * (c % ST);
-                if (!wait.one(&bar_w[c % ST], (uint32_t)(c / ST) & 1)) break;
-                tc_fence_after_sync();
+        const bool leader = elect_one();
+        const uint32_t id_up = idesc_bf16_f32(128, N, false, true);
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t b_tile = sb + (c % ST) * kStageBytes, w = tbase + TM_W - 128 * (c % ST);
+            if (!wait.warp(&bar_w[c % ST], (uint32_t)(c / ST) & 1)) break;
+            tc_fence_after_sync();
+            if (leader) {
                 issue_ts(tbase + TM_S, w, b_tile, id_up, c > 0);
                 issue_ts(tbase + TM_S, w + 64, b_tile, id_up, true);
                 mma_commit(&bar_upd[c % ST]);
                 mma_commit(&empty[c % ST]);
             }
+            __syncwarp();
+        }
+        if (leader) {
             mma_commit(&bar_drain);
             if (!mbar_wait(&bar_drain, 0, p.timeout_ns)) report_status(p.status, KDA_ERR_TIMEOUT);
         }
+        __syncwarp();
     } else if (warp < 4) {
         // the segment's state: the sum of its chunks, and for the first segment what is left of S0
         const Column<N, P> col(p, job, 32 * quarter + lane);
@@ -649,7 +668,7 @@ kda_ssm_state_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 0) tmem_dealloc(tbase, TM_COLS);
+    if (warp == 0) tmem_dealloc(tmem_base_s, TM_COLS);
 }
 
 // ------------------------------------------------------------------ outputs and states
@@ -662,13 +681,13 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_u32(smem_raw);
     uint8_t* sm = smem_raw + (((raw_base + 1023u) & ~1023u) - raw_base);
-    const uint32_t sb = smem_u32(sm);
+    const uint32_t sb = (raw_base + 1023u) & ~1023u;
     __shared__ Scalars scal[2];
-    __shared__ uint64_t full_x[kStages], full_bc, bar_scal[2], scal_free[2], bar_g, bar_cs, bar_upd, bar_px,
+    __shared__ uint64_t full_x[kStages], full_b, full_c, bar_scal[2], scal_free[2], bar_g, bar_cs, bar_upd, bar_px,
         bar_state, bar_w, bar_q, bar_yfree, bar_staged, bar_drain;
     __shared__ uint32_t tmem_base_s;
     __shared__ volatile int abort_s;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, quarter = warp & 3;
     Job job;
     if (!find_job<NH>(p, job)) return;
     const int chunks = job.chunks;
@@ -679,7 +698,8 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             mbar_init(&bar_scal[i], NH);
             mbar_init(&scal_free[i], kWorkers);
         }
-        mbar_init(&full_bc, 1);
+        mbar_init(&full_b, 1);
+        mbar_init(&full_c, 1);
         mbar_init(&bar_drain, 1);
         mbar_init(&bar_g, 1);
         mbar_init(&bar_cs, 1);
@@ -701,95 +721,125 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tbase = tmem_base_s;
+    constexpr uint32_t tbase = 0;            // all columns are this CTA's
     const Waiter wait{&abort_s, p.status, p.timeout_ns};
 
     if (warp == kLoadWarp) {
-        // ------------------------------------------------------------ loads of x and B, stores of y from the x tiles
-        if (lane == 0) {
-            int xs = 0, bs = 0;                                          // loads issued
-            auto x_in = [&](int c) {
-                if (c >= chunks) return;
+        // ------------------------------------------------------------ loads, and stores of y from the x tiles
+        const bool leader = elect_one();
+        int xs = 0, bs = 0, cs = 0;                                      // loads issued
+        auto x_in = [&](int c) {
+            if (c >= chunks) return;
+            if (leader) {
                 const int st = c % kStages;
                 mbar_arrive_expect_tx(&full_x[st], kTile);
                 load_x<NH>(sm + OFF_X + st * kTile, &tm_x, &full_x[st], job, job.row0 + c * kTok);
-                ++xs;
                 // x of the stage's next turn, which no other CTA reads, into L2
                 if (c + kStages < chunks) prefetch_x<NH>(&tm_x, job, job.row0 + (c + kStages) * kTok);
-            };
-            auto y_out = [&](int c) {
-                if (!wait.one(&bar_staged, c & 1)) return false;
-                if (!p.cu_seqlens || job.len - c * kTok >= kTok) {       // whole tiles, clipped at the end of the tensor
-                    for (int i = 0; i < 2; ++i)
-                        if (!(NH == 2 && i == 1 && job.h1 == job.h0))
-                            tma_store_4d(&tm_y, sm + OFF_X + (c % kStages) * kTile + i * ATOM, NH == 2 ? 0 : 64 * i,
-                                         NH == 2 && i ? job.h1 : job.h0, job.row0 + c * kTok, job.row_seq);
-                    bulk_commit_group();
-                    bulk_wait_read_all();
-                }
-                return true;
-            };
-            for (int c = 0; c < kStages - 1; ++c) x_in(c);
-            wait_for_launch_before();
-            bool ok = true;
-            for (int c = 0; c < chunks; ++c) {
-                // B and C are used up once the chunk before has updated the state (and all products before that have run)
-                if (c > 0 && !(ok = wait.one(&bar_upd, (uint32_t)(c - 1) & 1))) break;
-                mbar_arrive_expect_tx(&full_bc, 2 * kTile / 128 * N);
-                load_bc<N>(sm + OFF_B, &tm_b, &full_bc, job, job.row0 + c * kTok);
-                load_bc<N>(sm + OFF_C, &tm_c, &full_bc, job, job.row0 + c * kTok);
-                if (c + 1 < chunks) {
-                    prefetch_bc<N>(&tm_b, job, job.row0 + (c + 1) * kTok);
-                    prefetch_bc<N>(&tm_c, job, job.row0 + (c + 1) * kTok);
-                }
-                ++bs;
-                // a tile's next x follows once the y formed in its place has been read out
-                if (c > 0 && !(ok = y_out(c - 1))) break;
+            }
+            __syncwarp();
+            ++xs;
+        };
+        auto bc_in = [&](int c, uint32_t off, const CUtensorMap* tm, uint64_t* full, int& n) {
+            if (c >= chunks) return;
+            if (leader) {
+                mbar_arrive_expect_tx(full, kTile / 128 * N);
+                load_bc<N>(sm + off, tm, full, job, job.row0 + c * kTok);
+                if (c + 1 < chunks) prefetch_bc<N>(tm, job, job.row0 + (c + 1) * kTok);
+            }
+            __syncwarp();
+            ++n;
+        };
+        auto y_out = [&](int c) {
+            if (!wait.warp(&bar_staged, c & 1)) return false;
+            if (leader && (!p.cu_seqlens || job.len - c * kTok >= kTok)) {       // whole tiles, clipped at the end of the tensor
+                for (int i = 0; i < 2; ++i)
+                    if (!(NH == 2 && i == 1 && job.h1 == job.h0))
+                        tma_store_4d(&tm_y, sm + OFF_X + (c % kStages) * kTile + i * ATOM, NH == 2 ? 0 : 64 * i,
+                                     NH == 2 && i ? job.h1 : job.h0, job.row0 + c * kTok, job.row_seq);
+                bulk_commit_group();
+            }
+            __syncwarp();
+            return true;
+        };
+        bc_in(0, OFF_C, &tm_c, &full_c, cs);
+        bc_in(0, OFF_B, &tm_b, &full_b, bs);
+        for (int c = 0; c < kStages; ++c) x_in(c);
+        wait_for_launch_before();
+        for (int c = 0; c < chunks; ++c) {
+            // in the order in which their places become free
+            if (c > 0 && !y_out(c - 1)) break;
+            if (!wait.warp(&bar_cs, c & 1)) break;
+            bc_in(c + 1, OFF_C, &tm_c, &full_c, cs);
+            if (!wait.warp(&bar_upd, c & 1)) break;
+            bc_in(c + 1, OFF_B, &tm_b, &full_b, bs);
+            if (c > 0) {                                                 // x, once that y has been read out
+                if (leader) bulk_wait_read_all();
+                __syncwarp();
                 x_in(c + kStages - 1);
             }
-            if (ok && chunks > 0) (void)y_out(chunks - 1);
-            // nothing may be in flight when the CTA exits
-            bool done = bs == 0 || mbar_wait(&full_bc, (uint32_t)(bs - 1) & 1, p.timeout_ns);
+            if (c == chunks - 1) (void)y_out(c);
+        }
+        // nothing may be in flight when the CTA exits
+        if (leader) {
+            bool done = bs == 0 || mbar_wait(&full_b, (uint32_t)(bs - 1) & 1, p.timeout_ns);
+            done = (cs == 0 || mbar_wait(&full_c, (uint32_t)(cs - 1) & 1, p.timeout_ns)) && done;
             for (int c = max(0, xs - kStages); c < xs; ++c)
                 done = mbar_wait(&full_x[c % kStages], (uint32_t)(c / kStages) & 1, p.timeout_ns) && done;
             if (!done) report_status(p.status, KDA_ERR_TIMEOUT);
             bulk_wait_all();
         }
+        __syncwarp();
     } else if (warp == kIssueWarp) {
         // ------------------------------------------------------------ products
-        if (lane == 0) {
-            const uint32_t id_g = idesc_bf16_f32(128, 128, false, false);
-            const uint32_t id_cs = idesc_bf16_f32(128, kCols, false, false);
-            const uint32_t id_px = idesc_bf16_f32(128, P, false, true);
-            const uint32_t id_up = idesc_bf16_f32(128, N, false, true);
-            wait_for_launch_before();
-            for (int c = 0; c < chunks; ++c) {
-                const uint32_t par = c & 1;
-                // products run in order: G takes the place that Q X of the chunk before has read
-                if (!wait.one(&full_bc, par)) break;
-                tc_fence_after_sync();
+        // the whole warp, so that addresses stay in uniform registers; one thread issues
+        const bool leader = elect_one();
+        const uint32_t id_g = idesc_bf16_f32(128, 128, false, false);
+        const uint32_t id_cs = idesc_bf16_f32(128, kCols, false, false);
+        const uint32_t id_px = idesc_bf16_f32(128, P, false, true);
+        const uint32_t id_up = idesc_bf16_f32(128, N, false, true);
+        wait_for_launch_before();
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t par = c & 1;
+            // products run in order: G takes the place that Q X of the chunk before has read
+            if (!wait.warp(&full_c, par) || !wait.warp(&full_b, par)) break;
+            tc_fence_after_sync();
+            if (leader) {
                 issue_ss<N>(tbase + TM_G, sb + OFF_C, sb + OFF_B, id_g);
                 mma_commit(&bar_g);
-                if (!wait.one(&bar_state, par) || !wait.one(&bar_w, par)) break;   // S decayed and as bf16; the weighted x
-                tc_fence_after_sync();
+            }
+            __syncwarp();
+            if (!wait.warp(&bar_state, par) || !wait.warp(&bar_w, par)) break;   // S decayed and as bf16; the weighted x
+            tc_fence_after_sync();
+            if (leader) {
                 issue_ts(tbase + TM_S, tbase + TM_W, sb + OFF_B, id_up, true);
-                if (c > 0 && !wait.one(&bar_yfree, par ^ 1)) break;      // Y is free
-                tc_fence_after_sync();
+            }
+            __syncwarp();
+            if (c > 0 && !wait.warp(&bar_yfree, par ^ 1)) break;      // Y is free
+            tc_fence_after_sync();
+            if (leader) {
                 issue_ss<N>(tbase + TM_Y, sb + OFF_C, sb + OFF_S, id_cs);
                 mma_commit(&bar_cs);
                 issue_ts(tbase + TM_S, tbase + TM_W + 64, sb + OFF_B, id_up, true);
                 mma_commit(&bar_upd);
-                if (!wait.one(&bar_q, par)) break;                       // Q, and Y scaled
-                tc_fence_after_sync();
+            }
+            __syncwarp();
+            if (!wait.warp(&bar_q, par)) break;                          // Q, and Y scaled
+            tc_fence_after_sync();
+            if (leader) {
 #pragma unroll
                 for (int i = 0; i < NH; ++i)
                     issue_ts(tbase + TM_Y + i * P, tbase + TM_G + 64 * i,
                              sb + OFF_X + (c % kStages) * kTile + (NH == 2 ? i * ATOM : 0), id_px, true);
                 mma_commit(&bar_px);
             }
+            __syncwarp();
+        }
+        if (leader) {
             mma_commit(&bar_drain);
             if (!mbar_wait(&bar_drain, 0, p.timeout_ns)) report_status(p.status, KDA_ERR_TIMEOUT);
         }
+        __syncwarp();
     } else if (warp >= kDecayWarp) {
         // ------------------------------------------------------------ decays, up to two chunks ahead: a head to each warp, or
         // every other chunk
@@ -862,7 +912,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             const int n_valid = job.len - c * kTok;
             if (p.cu_seqlens && n_valid < kTok) {
                 // rows of other sequences, or of none: zeros, so that nothing of theirs enters a sum
-                (void)wait.warp(&full_bc, c & 1);
+                (void)wait.warp(&full_b, c & 1);
                 if (r >= n_valid && (part < 2 || part - 2 < N / 64)) {
                     uint8_t* row = sm + (part < 2 ? x_off + part * ATOM : OFF_B + (part - 2) * ATOM) + r * 128;
                     for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(row + i * 16) = make_uint4(0, 0, 0, 0);
@@ -1016,7 +1066,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 0) tmem_dealloc(tbase, TM_COLS);
+    if (warp == 0) tmem_dealloc(tmem_base_s, TM_COLS);
 }
 
 // [B, T, heads, d] bf16 with rows `ld` apart as a 4-D tensor (d, heads, T, B); box: 64 channels of one head, 128
