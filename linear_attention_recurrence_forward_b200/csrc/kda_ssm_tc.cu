@@ -243,7 +243,8 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t* u) {
                  : "memory");
 }
 
-// Bounded waits that also end when another warp of the CTA has given up.
+// Bounded waits of a whole warp, that also end when another warp of the CTA has given up.  The branch is the warp's,
+// not a lane's, and all lanes have the same answer.
 struct Waiter {
     volatile int* abort_flag;
     int* status;
@@ -252,25 +253,20 @@ struct Waiter {
     __device__ __noinline__ bool slow(uint32_t a, uint32_t parity) const {
         const uint64_t t0 = global_timer_ns();
         for (;;) {
-            if (*abort_flag) return false;
+            if (__any_sync(0xffffffffu, *abort_flag)) return false;
 #pragma unroll 1
             for (int i = 0; i < 32; ++i)
-                if (mbar_try_wait(a, parity)) return true;
-            if (global_timer_ns() - t0 > timeout_ns) {
+                if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+            if (__any_sync(0xffffffffu, global_timer_ns() - t0 > timeout_ns)) {
                 *abort_flag = 1;
                 report_status(status, KDA_ERR_TIMEOUT);
                 return false;
             }
         }
     }
-    // one thread
-    __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity) const {
-        const uint32_t a = smem_u32(bar);
-        return mbar_try_wait(a, parity) || slow(a, parity);
-    }
-    // a whole warp: the same answer in every lane
     __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
-        return __all_sync(0xffffffffu, one(bar, parity)) != 0;
+        const uint32_t a = smem_u32(bar);
+        return __all_sync(0xffffffffu, mbar_try_wait(a, parity)) || slow(a, parity);
     }
 };
 
