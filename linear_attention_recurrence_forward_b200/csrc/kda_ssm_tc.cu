@@ -285,8 +285,8 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 }
 
 // The second launch of a call may start while the first one runs: the first lets it once all of its CTAs are on their
-// SMs; the second sets itself up, starts its loads, and waits for the first one's end (and its writes).  4096 tokens,
-// 32 heads of 128: 55.5 us, one after the other 59.
+// SMs; the second sets itself up, starts its loads, and waits for the first one's end (and its writes).  At 4096
+// tokens and 32 heads of 128 that takes 3.5 us off 59.
 __device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
