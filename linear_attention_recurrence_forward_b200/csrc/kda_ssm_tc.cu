@@ -680,7 +680,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     const uint32_t sb = (raw_base + 1023u) & ~1023u;
     __shared__ Scalars scal[2];
     __shared__ uint64_t full_x[kStages], full_b, full_c, bar_scal[2], scal_free[2], bar_g, bar_cs, bar_upd, bar_px,
-        bar_state, bar_w, bar_q, bar_yfree, bar_staged, bar_drain;
+        bar_state, bar_w, bar_q, bar_yfree, bar_staged[2], bar_drain;
     __shared__ uint32_t tmem_base_s;
     __shared__ volatile int abort_s;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, quarter = warp & 3;
@@ -693,6 +693,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar_scal[i], NH);
             mbar_init(&scal_free[i], kWorkers);
+            mbar_init(&bar_staged[i], kWorkers);
         }
         mbar_init(&full_b, 1);
         mbar_init(&full_c, 1);
@@ -705,7 +706,6 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         mbar_init(&bar_w, kWorkers);
         mbar_init(&bar_q, kWorkers);
         mbar_init(&bar_yfree, kWorkers);
-        mbar_init(&bar_staged, kWorkers);
         fence_mbar_init();
         abort_s = 0;
         prefetch_tensormap(&tm_x); prefetch_tensormap(&tm_b); prefetch_tensormap(&tm_c); prefetch_tensormap(&tm_y);
@@ -747,7 +747,9 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             ++n;
         };
         auto y_out = [&](int c) {
-            if (!wait.warp(&bar_staged, c & 1)) return false;
+            // two barriers in turn: the last chunk's y may be in place before y of the one before is looked for (what
+            // comes after that needs loads of this warp's)
+            if (!wait.warp(&bar_staged[c & 1], (uint32_t)(c >> 1) & 1)) return false;
             if (leader && (!p.cu_seqlens || job.len - c * kTok >= kTok)) {       // whole tiles, clipped at the end of the tensor
                 for (int i = 0; i < 2; ++i)
                     if (!(NH == 2 && i == 1 && job.h1 == job.h0))
@@ -1049,7 +1051,7 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 }
             }
             fence_proxy_async_smem();
-            warp_arrive(&bar_staged, lane);
+            warp_arrive(&bar_staged[par], lane);
         }
         // the state after the sequence's last token
         if (chunks > 0 && job.last && p.ST && wait.warp(&bar_upd, (uint32_t)(chunks - 1) & 1) && has_rows && !abort_s) {

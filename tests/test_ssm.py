@@ -374,6 +374,30 @@ def test_segments_packed():
 
 
 @gpu
+@pytest.mark.parametrize("P", [64, 128])
+def test_many_short_prompts_beside_heavy_traffic(P):
+    """Hundreds of calls over short packed prompts while another stream copies: loads and stores take long there, and
+    no wait of the kernel may mistake one chunk's arrival for another's."""
+    lengths = [1, 130, 257, 384, 511, 640, 90, 256] * 3
+    T = sum(lengths)
+    c = case((T,), 24, 2, 128, P, "bf16", seed=11, states=len(lengths))
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device="cuda")
+    want = kda.kda_ssm_forward_varlen(**c, cu_seqlens=cu)
+    a, b = (torch.empty(1 << 28, dtype=torch.uint8, device="cuda") for _ in range(2))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for i in range(300):
+        if i % 4 == 0:
+            with torch.cuda.stream(side):
+                b.copy_(a)
+        got = kda.kda_ssm_forward_varlen(**c, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    assert kda.kda_get_device_status() == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@gpu
 def test_a_wait_that_runs_out_is_reported():
     c = case((1, 300), 2, 1, 128, 64, "bf16", seed=8)
     want = kda.kda_ssm_forward(**c)
