@@ -50,9 +50,10 @@
 // the second starts each segment from the segments before it, S <- 2^{total} S + local, folded in as it
 // loads its start state.
 //
-// No barrier completes twice before its waiter has looked (the parity would then stand for the phase before): each
-// next phase needs something that the waiter does after its wait.  Every wait is bounded in time; a wait that runs out sets the status word and an abort flag that ends
-// the other warps' waits, the products and loads in flight are drained, and the CTA returns.
+// No barrier completes twice before its waiter has looked (the parity would then stand for the phase before):
+// each next phase needs something that the waiter does after its wait.  Every wait is bounded in time; a wait
+// that runs out sets the status word and an abort flag that ends the other warps' waits, the products and
+// loads in flight are drained, and the CTA returns.
 #include <cudaTypedefs.h>
 #include <mutex>
 
