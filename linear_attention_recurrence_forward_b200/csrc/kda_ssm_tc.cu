@@ -862,9 +862,10 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             float step[4], incl[4], after[4], total[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                step[k] = c * kTok + 32 * k + lane < job.len
-                              ? softplus(__bfloat162float(__ushort_as_bfloat16(raw[k])) + bias) : 0.f;
-                block_sums(fmaxf(step[k] * rate, kLeastDecay), lane, incl[k], after[k]);
+                const bool in = c * kTok + 32 * k + lane < job.len;
+                step[k] = in ? softplus(__bfloat162float(__ushort_as_bfloat16(raw[k])) + bias) : 0.f;
+                // past the last token nothing decays, at a rate of -infinity too
+                block_sums(in ? fmaxf(step[k] * rate, kLeastDecay) : 0.f, lane, incl[k], after[k]);
                 total[k] = __shfl_sync(0xffffffffu, incl[k], 31);
             }
             load_dt(n + 2);

@@ -472,3 +472,15 @@ def test_convolution_feeds_the_kda_prefill():
     o, S = kda.kda_forward_chunked_fused(q, k, v, zg, zb)
     o_ref, S_ref = oracle.forward_fused(q, k, v, zg, zb)
     assert max_rel_err(np64(o), o_ref) <= 2e-2 and max_rel_err(np64(S), S_ref) <= 2e-2
+
+
+@gpu
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+@pytest.mark.parametrize("T", [1, 130, 256, 2050])
+def test_a_rate_of_minus_infinity_forgets_everything(dtype, impl, T):
+    """A = -infinity: every token starts from nothing.  The rows after the last token do not decay its state."""
+    c = case((1, T), 3, 1, 128, 64, dtype, seed=4)
+    c["A"][1] = -float("inf")
+    y, S = kda.kda_ssm_forward(**c, impl=impl)
+    assert kda.kda_get_device_status() == 0
+    check(y[0], S[0], c, 0, 0, dtype, impl)
