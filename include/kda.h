@@ -461,7 +461,8 @@ KDA_API int kda_short_conv_step_paged(const void* x, const void* weight, const v
  *             aligned (NULL when that is 0), not used by anything else until the work is done.
  *
  * The tensor-core kernel forms whole 128-token blocks: a non-finite value in one token's x, B or dt
- * may reach the outputs of other tokens of its block, earlier ones too.  T == 0 copies S0 to S_T.
+ * may reach the outputs of other tokens of its block, earlier ones too.  A NaN in A[h] makes head h's
+ * outputs and state NaN; A[h] = -infinity forgets everything before each token.  T == 0 copies S0 to S_T.
  */
 KDA_API int kda_ssm_forward(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
                             const float* D, const float* dt_bias, const float* S0, void* y, float* S_T, int B,

@@ -864,8 +864,10 @@ kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             for (int k = 0; k < 4; ++k) {
                 const bool in = c * kTok + 32 * k + lane < job.len;
                 step[k] = in ? softplus(__bfloat162float(__ushort_as_bfloat16(raw[k])) + bias) : 0.f;
-                // past the last token nothing decays, at a rate of -infinity too
-                block_sums(in ? fmaxf(step[k] * rate, kLeastDecay) : 0.f, lane, incl[k], after[k]);
+                // compared, so that a NaN stays one (fmaxf would drop it); past the last token nothing decays, at a
+                // rate of -infinity too
+                const float la = step[k] * rate;
+                block_sums(in ? (la < kLeastDecay ? kLeastDecay : la) : 0.f, lane, incl[k], after[k]);
                 total[k] = __shfl_sync(0xffffffffu, incl[k], 31);
             }
             load_dt(n + 2);

@@ -476,6 +476,21 @@ def test_convolution_feeds_the_kda_prefill():
 
 @gpu
 @pytest.mark.parametrize("dtype,impl", IMPLS)
+@pytest.mark.parametrize("T,P", [(130, 64), (130, 128), (2048, 64), (2048, 128)])
+def test_a_rate_of_nan_shows(dtype, impl, T, P):
+    """A NaN in one head's A makes all of that head's outputs and its state NaN, in short prompts and in long ones
+    that are cut into segments, and leaves the other heads as they were."""
+    c = case((1, T), 3, 1, 128, P, dtype, seed=2)
+    want, want_S = kda.kda_ssm_forward(**c, impl=impl)
+    c["A"] = c["A"].clone()
+    c["A"][1] = float("nan")
+    y, S = kda.kda_ssm_forward(**c, impl=impl)
+    assert bool(y[:, :, 1].isnan().all()) and bool(S[:, 1].isnan().all())
+    assert torch.equal(y[:, :, ::2], want[:, :, ::2]) and torch.equal(S[:, ::2], want_S[:, ::2])
+
+
+@gpu
+@pytest.mark.parametrize("dtype,impl", IMPLS)
 @pytest.mark.parametrize("T", [1, 130, 256, 2050])
 def test_a_rate_of_minus_infinity_forgets_everything(dtype, impl, T):
     """A = -infinity: every token starts from nothing.  The rows after the last token do not decay its state."""
