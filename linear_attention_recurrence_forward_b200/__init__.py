@@ -824,12 +824,23 @@ def kda_ssm_decode_step_paged(x, dt, A, Bm, Cm, S_pool, slots, D=None, dt_bias=N
     return y
 
 
+def _dense_from(t) -> int:
+    """The first dimension, 1 or later, from which on a pool tensor is one contiguous run."""
+    shape, stride = t.shape, t.stride()
+    run, d = 1, len(shape)
+    while d > 1 and (stride[d - 1] == run or shape[d - 1] == 1):
+        d -= 1
+        run *= shape[d]
+    return d
+
+
 def _pools(pools, name: str, device=None, beside=None):
     """The kda_pool descriptions of a list of pool tensors [n_slots, ...]: (their bytes, number of slots, device).
 
-    Dimension 0 counts the slots.  The others are contiguous, or dimension 1 is spaced wider (the boundary
-    states of one batch entry, S_mid[b].transpose(0, 1) of kda_forward_chunked_states).  A pool whose
-    counterpart in `beside` is spaced wider is described by the same runs."""
+    Dimension 0 counts the slots and may be spaced wider than a slot.  The others are contiguous, or dimension 1
+    is spaced wider (the boundary states of one batch entry, S_mid[b].transpose(0, 1) of
+    kda_forward_chunked_states).  A pool whose counterpart in `beside` is split along dimension 1 is split there
+    too, so that both are described by the same runs."""
     if not pools:
         raise ValueError(f"{name} is empty")
     flat, n_slots = [], pools[0].shape[0]
@@ -845,18 +856,14 @@ def _pools(pools, name: str, device=None, beside=None):
             slot = t.nbytes // n_slots if n_slots else 0
             flat += (t.data_ptr(), slot, 1, 0, slot)
             continue
-        stride, es = t.stride(), t.element_size()
-        run, d = 1, len(shape) - 1
-        last = 1 if beside is not None and len(shape) > 2 and not beside[i].is_contiguous() else 0
-        while d > last and (stride[d] == run or shape[d] == 1):
-            run *= shape[d]
-            d -= 1
-        if d == 0:
-            pieces, apart = 1, 0
-        elif d == 1:
-            pieces, apart = shape[1], stride[1]
-        else:
+        first = _dense_from(t)
+        if first > 2:
             raise ValueError(f"{name}: a pool's slots must be contiguous, or contiguous runs along dimension 1")
+        if beside is not None:
+            first = max(first, min(_dense_from(beside[i]), 2))
+        stride, es = t.stride(), t.element_size()
+        run = math.prod(shape[first:])
+        pieces, apart = (1, 0) if first == 1 else (shape[1], stride[1])
         flat += (t.data_ptr(), (stride[0] if n_slots > 1 else max(stride[0], run)) * es, pieces, apart * es, run * es)
     return struct.pack(f"{len(flat)}q", *flat), n_slots, device
 

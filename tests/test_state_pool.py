@@ -246,3 +246,47 @@ def test_in_a_graph():
     kda.kda_pool_copy(ref_pools, src, dst)
     want = kda.kda_pool_compact(ref_pools, table)
     assert torch.equal(new, want) and all(torch.equal(p, r) for p, r in zip(pools, ref_pools))
+
+
+# ---------------------------------------------------------------------- pools with slots apart
+
+def pairs_of_layouts(device):
+    """Pools of six slots [3, 8, 16], one element type, in the layouts the binding takes: (name, tensor)."""
+    z = lambda *s: torch.zeros(*s, device=device)  # noqa: E731
+    return [("contiguous", z(6, 3, 8, 16)),
+            ("slots of one layer of several", z(6, 2, 3, 8, 16)[:, 1]),
+            ("every other slot", z(12, 3, 8, 16)[::2]),
+            ("runs apart", z(3, 9, 8, 16).transpose(0, 1)[:6])]
+
+
+@pytest.mark.parametrize("a", range(4))
+@pytest.mark.parametrize("b", range(4))
+def test_layouts_of_a_pool_and_its_source_agree(L, a, b):
+    """Any two layouts of the same slots are described by the same runs, in both directions, and only split into
+    runs where one of the two needs it."""
+    (name, to), (_, frm) = pairs_of_layouts("cpu")[a], pairs_of_layouts("cpu")[b]
+    d, n_dst, dev = kda._pools([to], "pools", beside=[frm])
+    s, n_src, _ = kda._pools([frm], "src_pools", dev, beside=[to])
+    assert L.kda_pool_copy(d, s, 1, n_dst, n_src, IX, IX + 64, 0, None) == OK, name
+    one_run = 3 not in (a, b)
+    for t, bytes_ in ((to, d), (frm, s)):
+        base, slot, pieces, apart, run = np.frombuffer(bytes_, np.int64).tolist()
+        assert (base, slot) == (t.data_ptr(), t.stride(0) * 4)
+        assert (pieces, run) == ((1, 3 * 8 * 16 * 4) if one_run else (3, 8 * 16 * 4))
+        assert one_run or apart == t.stride(1) * 4
+
+
+@gpu
+@pytest.mark.parametrize("a", range(4))
+@pytest.mark.parametrize("b", range(4))
+def test_copy_between_layouts(a, b):
+    to, frm = pairs_of_layouts("cuda")[a][1], pairs_of_layouts("cuda")[b][1]
+    whole = to._base if to._base is not None else to
+    whole.fill_(7.0)
+    frm.copy_(torch.randn(frm.shape, device="cuda"))
+    want = whole.clone()
+    view = want.as_strided(to.shape, to.stride(), to.storage_offset())
+    view[4], view[0] = frm[1], frm[5]
+    kda.kda_pool_copy([to], ids([1, 5, -1]), ids([4, 0, 2]), src_pools=[frm])
+    assert kda.kda_get_device_status() == 0
+    assert torch.equal(whole, want)                  # what lies between the slots too
