@@ -530,12 +530,13 @@ typedef struct {
  *   dst, src         : HOST arrays of n_pools pools; dst[p] and src[p] have the same pieces and
  *                      piece_bytes, and are the same pool or do not overlap
  *   n_dst, n_src     : slots of every dst and every src pool
- *   src_idx, dst_idx : [n] int32 DEVICE arrays; a pair with a negative index is skipped
+ *   src_idx, dst_idx : [n] int32 DEVICE arrays, n at most 2^20; a pair with a negative index is skipped
  *
  * A pair is not copied, and the status word is set to KDA_ERR_INVALID_ARG, when an index is past its
  * pool, when another pair has the same destination, or when (dst[p] being src[p]) its destination is
  * the source of another pair: the result never depends on the order of the copies.  A pair of a slot
- * with itself does nothing.
+ * with itself does nothing.  Finding such pairs costs one reading of the list for each 512 pairs of it (for
+ * each pair up to 1024 pairs): 3 ms for 65536 pairs in 16 pools, which is long only beside small slots.
  */
 KDA_API int kda_pool_copy(const kda_pool* dst, const kda_pool* src, int n_pools, int n_dst, int n_src,
                           const int* src_idx, const int* dst_idx, int n, struct CUstream_st* stream);

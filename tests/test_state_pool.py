@@ -290,3 +290,62 @@ def test_copy_between_layouts(a, b):
     kda.kda_pool_copy([to], ids([1, 5, -1]), ids([4, 0, 2]), src_pools=[frm])
     assert kda.kda_get_device_status() == 0
     assert torch.equal(whole, want)                  # what lies between the slots too
+
+
+# ---------------------------------------------------------------------- many pairs
+
+@gpu
+@pytest.mark.parametrize("n", [1023, 1024, 1025, 5000, 40000])
+@pytest.mark.parametrize("within", [True, False])
+def test_many_pairs_with_conflicts(n, within):
+    """Lists of more than 1024 pairs: destinations that come twice, are read, or lie past the pool, far apart in the
+    list, are left out; all others are copied."""
+    rng = np.random.RandomState(n)
+    n_slots = 3 * n
+    order = rng.permutation(n_slots)
+    src, dst = order[:n].copy(), order[n:2 * n].copy()
+    for _ in range(8):
+        a, b = rng.choice(n, 2, replace=False)
+        dst[a] = dst[b]                                    # one destination twice
+        a, b = rng.choice(n, 2, replace=False)
+        src[a] = dst[b]                                    # a destination that another pair reads
+        dst[rng.randint(n)] = n_slots + rng.randint(100)   # past the pool
+        src[rng.randint(n)] = n_slots + rng.randint(100)
+        dst[rng.randint(n)] = -1
+        a = rng.randint(n)
+        src[a] = dst[a]                                    # a slot with itself
+    pools = [torch.arange(n_slots * k, dtype=torch.int32, device="cuda").reshape(n_slots, k) for k in (4, 12)]
+    source = None if within else [p + 1000000 for p in pools]
+    frm = [p.clone() for p in (pools if within else source)]
+    want = [p.clone() for p in pools]
+    kda.kda_pool_copy(pools, ids(src), ids(dst), src_pools=source)
+    used = (src >= 0) & (dst >= 0)
+    times = np.bincount(dst[used], minlength=n_slots + 100)
+    read = np.zeros(n_slots + 100, bool)
+    read[src[used]] = True
+    fine = used & (src < n_slots) & (dst < n_slots) & (times[np.maximum(dst, 0)] == 1)
+    if within:
+        fine &= (src == dst) | ~read[np.maximum(dst, 0)]
+    s, d = (torch.tensor(t[fine], device="cuda") for t in (src, dst))
+    for p, f, w in zip(pools, frm, want):
+        w[d] = f[s]
+        assert torch.equal(p, w)
+    assert kda.kda_get_device_status() == INVALID          # some were left out
+
+
+@gpu
+def test_the_check_of_many_pairs_is_short():
+    """65536 pairs in 16 pools of small slots: the check does not compare every pair with every other for each pool
+    (100 ms when it did)."""
+    n = 65536
+    pools = [torch.zeros(2 * n, 64, device="cuda") for _ in range(16)]
+    order = torch.randperm(2 * n, device="cuda").to(torch.int32)
+    src, dst = order[:n].contiguous(), order[n:].contiguous()
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    kda.kda_pool_copy(pools, src, dst)
+    start.record()
+    kda.kda_pool_copy(pools, src, dst)
+    end.record()
+    end.synchronize()
+    assert kda.kda_get_device_status() == 0
+    assert start.elapsed_time(end) < 20
