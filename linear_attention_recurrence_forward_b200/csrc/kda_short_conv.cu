@@ -7,8 +7,9 @@
 // L2 hits: the strip above is in flight), and loads 16 (fp32: 8) rows before it uses the first.  In bf16
 // the arithmetic is nearly as long as the traffic: the f32x2 instructions take two channels at once,
 // and four channels a thread keep registers low enough for five blocks an SM.  One B200, 16384 x 12288
-// bf16 with SiLU: 150 us (0.82 of the measured copy rate; 127 us without the activation); eight
-// channels a thread with 16-byte loads 159 us, scalar arithmetic 222 us; fp32 254 us (0.97).
+// bf16 with SiLU: 150 to 154 us (0.80 to 0.82 of the measured copy rate; 127 to 129 us without the
+// activation); eight channels a thread with 16-byte loads 159 us, scalar arithmetic 222 us; fp32 262 us (0.94;
+// 252 us without the activation).
 //
 // The first W-1 tokens of a sequence, which need the state, and the state after its last token belong
 // to blocks of their own, one per sequence and channel range: those read everything before they write
@@ -80,9 +81,10 @@ __device__ __forceinline__ void pack(const uint64_t (&f)[2], uint2& r) {
     r = make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
 }
 
-// v / (1 + 2^(-v log2 e)), both lanes: the hardware exponential and reciprocal, each off by about 2^-22, and the
-// exponent's rounding, 2^-24 of it (all far below a bf16 step; for fp32 a few units in the last place)
-__device__ __forceinline__ uint64_t silu2(uint64_t v) {
+// SiLU of both lanes for bf16 outputs: v / (1 + 2^(-v log2 e)) by the hardware exponential and reciprocal.  Each is off
+// by about 2^-22, and the exponent's rounding by |v log2 e| 2^-24 of the result, 2^-17 at most: far below half a bf16
+// step of 2^-8.  Below -87.3, where the reciprocal has no normal value, the result is zero (exact: under 1e-36).
+__device__ __forceinline__ uint64_t silu2(uint64_t v, __nv_bfloat16) {
     const float2 a = split2(mul2(v, pair2(-1.4426950408889634f, -1.4426950408889634f)));
     float ex, ey, rx, ry;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ex) : "f"(a.x));
@@ -91,6 +93,29 @@ __device__ __forceinline__ uint64_t silu2(uint64_t v) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rx) : "f"(d.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ry) : "f"(d.y));
     return mul2(v, pair2(rx, ry));
+}
+// And for fp32 outputs: with e = exp(-|v|), v / (1 + e) or, below zero, v e / (1 + e); nothing overflows.  e is
+// 2^p' (1 + r ln 2): p' the rounded product of -|v| and log2 e, r what the rounding left out, which a fused multiply-add
+// gives exactly, and the low part of log2 e.  Off by 10 * 2^-24 of the value at most: 4 from the exponential, 2 from the
+// reciprocal, one from each of four roundings.  16384 x 12288: 262 us, with expf and a division 350 us, with the bf16
+// form (57 to 80 * 2^-24 off between -20 and -87, zero below) 256 us.
+__device__ __forceinline__ uint64_t silu2(uint64_t v, float) {
+    constexpr float kLog2e = 1.44269504f, kLog2eLow = (float)(1.4426950408889634 - (double)kLog2e);
+    const float2 x = split2(v);
+    const uint64_t mag = pair2(fminf(fabsf(x.x), 128.f), fminf(fabsf(x.y), 128.f));     // e is zero from there on
+    const uint64_t p = mul2(mag, pair2(kLog2e, kLog2e));
+    uint64_t r = fma2(mag, pair2(-kLog2e, -kLog2e), p);
+    r = fma2(mag, pair2(-kLog2eLow, -kLog2eLow), r);
+    const float2 q = split2(p);
+    float ex, ey, rx, ry;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(ex) : "f"(-q.x));
+    asm("ex2.approx.f32 %0, %1;" : "=f"(ey) : "f"(-q.y));
+    uint64_t e = pair2(ex, ey);
+    e = fma2(e, mul2(r, pair2(0.69314718f, 0.69314718f)), e);
+    const float2 d = split2(add2(e, pair2(1.f, 1.f))), w = split2(e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rx) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ry) : "f"(d.y));
+    return mul2(mul2(v, pair2(x.x < 0.f ? w.x : 1.f, x.y < 0.f ? w.y : 1.f)), pair2(rx, ry));
 }
 
 // Weights and bias of a thread's channels, and the filter applied to a window of inputs.
@@ -146,7 +171,7 @@ struct Filter {
         }
         if (act) {
 #pragma unroll
-            for (int j = 0; j < H; ++j) out[j] = silu2(out[j]);
+            for (int j = 0; j < H; ++j) out[j] = silu2(out[j], T());
         }
         R r;
         pack(out, r);

@@ -268,3 +268,27 @@ def test_extreme_values():
     x[0, 10] = float("inf")
     y, _ = kda.kda_short_conv(x, rand((64, 4), "bf16", 2))
     assert bool(torch.isfinite(y[0, :10].float()).all()) and bool(torch.isfinite(y[0, 14:].float()).all())
+
+
+@gpu
+@pytest.mark.parametrize("step", [False, True])
+def test_fp32_activation_to_the_last_places(step):
+    """SiLU of single values in fp32, relative to each value: the exponential (2^-22), its correction, a product,
+    a sum and the last product (2^-24 each) and the reciprocal (2^-23) make 10 * 2^-24; below the normal numbers
+    the exponential is off by up to 4 of the smallest steps, 2^-149, times the value."""
+    v = torch.cat([torch.linspace(-104, 90, 40000, device="cuda"), torch.linspace(-1, 1, 9992, device="cuda"),
+                   torch.tensor([0.0, -0.0, 1e-30, -1e-30, 3e38, -3e38, -87.4, -88.8], device="cuda")])
+    w = torch.zeros(8, 4, device="cuda")
+    w[:, 3] = 1
+    x = v.reshape(1, -1, 8)
+    if step:
+        y = kda.kda_short_conv_step(x[0], w, torch.zeros(x.shape[1], 3, 8, device="cuda"))
+    else:
+        y, _ = kda.kda_short_conv(x, w)
+    z = np64(v)
+    e = np.exp(-np.abs(z))
+    ref_y = np.where(z < 0, z * e, z) / (1 + e)
+    err = np.abs(np64(y).ravel() - ref_y)
+    assert np.all(err <= 10 * 2.0 ** -24 * np.abs(ref_y) + 2.0 ** -147 * (1 + np.abs(z))), float((err / np.abs(ref_y + 1e-300)).max())
+    assert bool(torch.isnan(kda.kda_short_conv(torch.full((1, 1, 8), float("nan"), device="cuda"), w)[0]).all())
+    assert bool((kda.kda_short_conv(torch.full((1, 1, 8), float("inf"), device="cuda"), w)[0] == float("inf")).all())
