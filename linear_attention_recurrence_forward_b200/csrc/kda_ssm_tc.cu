@@ -1182,12 +1182,7 @@ size_t ssm_tc_workspace(int n_seq, long long T_total, int H, int N, int P) {
 
 cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t s) {
     const int B = a.cu_seqlens ? 1 : a.n_seq;
-    if (a.T == 0) {
-        // packed sequences without tokens: S_T = S0
-        if (!a.ST || a.ST == a.S0) return cudaSuccess;
-        const size_t bytes = (size_t)a.n_seq * a.H * a.N * a.P * sizeof(float);
-        return a.S0 ? cudaMemcpyAsync(a.ST, a.S0, bytes, cudaMemcpyDeviceToDevice, s) : cudaMemsetAsync(a.ST, 0, bytes, s);
-    }
+    if (a.T == 0) return launch_ssm_simt(a, s);      // packed sequences without tokens: the offsets' check and S_T = S0
     CUtensorMap mx, mb, mc, my;
     if (!make_map(&mx, a.x, B, a.T, a.H, a.P, a.ldx) || !make_map(&mb, a.Bm, B, a.T, a.G, a.N, a.ldb) ||
         !make_map(&mc, a.Cm, B, a.T, a.G, a.N, a.ldc) || !make_map(&my, a.y, B, a.T, a.H, a.P, (long long)a.H * a.P))

@@ -499,3 +499,22 @@ def test_a_rate_of_minus_infinity_forgets_everything(dtype, impl, T):
     y, S = kda.kda_ssm_forward(**c, impl=impl)
     assert kda.kda_get_device_status() == 0
     check(y[0], S[0], c, 0, 0, dtype, impl)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+@pytest.mark.parametrize("offsets,status", [([0, 0, 0], OK), ([0, 5, 3], INVALID), ([0, 0, 1], INVALID), ([-1, 0, 0], INVALID)])
+def test_packed_without_tokens(dtype, impl, offsets, status):
+    """No tokens at all: the states pass through, and offsets that promise some are reported."""
+    c = case((0,), 2, 1, 64, 128, dtype, states=2)
+    cu = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    y, S = kda.kda_ssm_forward_varlen(**c, cu_seqlens=cu, impl=impl)
+    assert kda.kda_get_device_status() == status
+    assert y.shape == (0, 2, 128) and torch.equal(S, c["S0"])
+    _, S = kda.kda_ssm_forward_varlen(**{**c, "S0": None}, cu_seqlens=cu, impl=impl)
+    assert kda.kda_get_device_status() == status and bool((S == 0).all())
+    held = c["S0"].clone()
+    kda.kda_ssm_forward_varlen(**{**c, "S0": held}, cu_seqlens=cu, impl=impl, S_T=held)
+    assert kda.kda_get_device_status() == status and torch.equal(held, c["S0"])
+    kda.kda_ssm_forward_varlen(**c, cu_seqlens=cu, impl=impl, return_state=False)
+    assert kda.kda_get_device_status() == status
