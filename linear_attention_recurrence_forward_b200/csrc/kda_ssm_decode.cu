@@ -93,8 +93,10 @@ kda_ssm_decode_kernel(const T* __restrict__ x, const T* __restrict__ dt, const f
             const float4 t = red[w][tid];
             o.x += t.x; o.y += t.y; o.z += t.z; o.w += t.w;
         }
-        const float d = D ? D[h] : 0.f;       // this thread's columns: tid == c4
-        o.x = fmaf(d, xv.x, o.x); o.y = fmaf(d, xv.y, o.y); o.z = fmaf(d, xv.z, o.z); o.w = fmaf(d, xv.w, o.w);
+        if (D) {                              // this thread's columns: tid == c4
+            const float d = D[h];
+            o.x = fmaf(d, xv.x, o.x); o.y = fmaf(d, xv.y, o.y); o.z = fmaf(d, xv.z, o.z); o.w = fmaf(d, xv.w, o.w);
+        }
         store4(y + bh * P + col, o);
     }
 }

@@ -158,8 +158,8 @@ kda_ssm_simt_kernel(const T* __restrict__ x, const T* __restrict__ dt, const flo
         if (rl < n) {
             const float2 xv = *reinterpret_cast<const float2*>(&xs[buf][rl][cl]);
             const size_t o = ((base + t0 + rl) * H + h) * P + col0 + cl;
-            store_elem(y, o, fmaf(skip, xv.x, yp[0][0]));
-            store_elem(y, o + 1, fmaf(skip, xv.y, yp[0][1]));
+            store_elem(y, o, D ? fmaf(skip, xv.x, yp[0][0]) : yp[0][0]);
+            store_elem(y, o + 1, D ? fmaf(skip, xv.y, yp[0][1]) : yp[0][1]);
         }
     }
     if (!ST) return;

@@ -518,3 +518,25 @@ def test_packed_without_tokens(dtype, impl, offsets, status):
     assert kda.kda_get_device_status() == status and torch.equal(held, c["S0"])
     kda.kda_ssm_forward_varlen(**c, cu_seqlens=cu, impl=impl, return_state=False)
     assert kda.kda_get_device_status() == status
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("N,P", [(64, 64), (128, 128)])
+def test_no_skip_term_adds_nothing_to_infinities(dtype, N, P):
+    """Without D there is no D x: an infinite x among positive B and C makes its column's outputs infinite from that
+    token on, not 0 times infinity.  Token-serial kernel and single tokens."""
+    c = case((1, 5), 2, 1, N, P, dtype, seed=6)
+    del c["D"]
+    for k in ("x", "Bm", "Cm", "S0"):
+        c[k] = c[k].abs() + 0.125
+    c["x"][0, 2, 1, 7] = float("inf")
+    y, S = kda.kda_ssm_forward(**c, impl="simt")
+    held = c["S0"].clone()
+    steps = [kda.kda_ssm_decode_step(c["x"][:, t], c["dt"][:, t], c["A"], c["Bm"][:, t], c["Cm"][:, t], held, None, c["dt_bias"])
+             for t in range(5)]
+    for out, state in ((y, S), (torch.stack(steps, 1), held)):
+        inf = torch.zeros(1, 5, 2, P, dtype=torch.bool, device="cuda")
+        inf[0, 2:, 1, 7] = True
+        assert torch.equal(out == float("inf"), inf) and bool(out[~inf].isfinite().all())
+        assert bool((state[0, 1, :, 7] == float("inf")).all()) and int(state.isfinite().sum()) == state.numel() - N
