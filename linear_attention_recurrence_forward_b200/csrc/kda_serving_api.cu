@@ -151,6 +151,7 @@ int run_ssm(kda::SsmArgs& a, size_t tokens, int impl, size_t workspace_bytes, cu
 
 constexpr int kMostPools = 512;
 constexpr int kMostIndices = 1 << 20;
+constexpr double kMostSlotBytes = 1.0e13;
 
 size_t pool_bytes(const kda_pool& p, int n_slots) {
     return (size_t)(n_slots - 1) * p.slot_stride + (size_t)(p.pieces - 1) * p.piece_stride + p.piece_bytes;
@@ -160,6 +161,9 @@ int check_pool(const kda_pool& p, int n_slots) {
     if (!p.base || p.pieces <= 0 || p.piece_bytes <= 0 || p.slot_stride < p.piece_bytes || p.pieces > (1 << 20) ||
         p.piece_bytes > (1ll << 40) || p.slot_stride > kMostStride || p.piece_stride > kMostStride ||
         (p.pieces > 1 && p.piece_stride < p.piece_bytes))
+        return KDA_ERR_INVALID_ARG;
+    // sizes and distances far from overflow: those of the pool in 64 bits, the parts of a slot in 32
+    if ((double)n_slots * (double)p.slot_stride > kMostElements || (double)p.pieces * (double)p.piece_bytes > kMostSlotBytes)
         return KDA_ERR_INVALID_ARG;
     if (!aligned16(p.base) || p.slot_stride % 16 != 0 || p.piece_bytes % 16 != 0 ||
         (p.pieces > 1 && p.piece_stride % 16 != 0))

@@ -349,3 +349,18 @@ def test_the_check_of_many_pairs_is_short():
     end.synchronize()
     assert kda.kda_get_device_status() == 0
     assert start.elapsed_time(end) < 20
+
+
+# ---------------------------------------------------------------------- pools beyond any memory
+
+def test_sizes_that_overflow_are_refused(L):
+    """A pool whose size does not fit 64 bits would pass for a small one: its slots and the indices, or another pool,
+    would seem apart."""
+    stride = 1 << 40
+    far = desc((BASE, stride, 1, 0, 1024))
+    n = (1 << 24) + 1                                                   # the last slot wraps around to the first
+    assert L.kda_pool_clear(far, 1, n, BASE + stride, 4, None) == INVALID
+    assert L.kda_pool_copy(far, desc((BASE + stride, 1024, 1, 0, 1024)), 1, n, 8, IX, IX + 64, 4, None) == INVALID
+    assert L.kda_pool_clear(far, 1, 2 ** 31 - 1, IX, 0, None) == INVALID
+    assert L.kda_pool_clear(desc((BASE, stride, 1 << 20, 1 << 26, 1 << 26)), 1, 1, IX, 0, None) == INVALID
+    assert L.kda_pool_clear(desc((BASE, 1 << 38, 1, 0, 1 << 38)), 1, 16, IX + (1 << 44), 0, None) == OK
