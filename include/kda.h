@@ -605,7 +605,8 @@ KDA_API int kda_version(void);
  *   mode 1: subsequent tcgen05 prefill launches skip the first hand-off from the operand
  *           warps to the recurrence warps, so a wait is guaranteed to run out; every wait
  *           is limited to timeout_ns (1 ms .. 10 s).  Outputs of such launches are undefined.
- *           Tensor-core launches of the selective scan skip their first hand-off too.
+ *           Tensor-core calls of the selective scan skip their first hand-off too (where a prompt is
+ *           cut into segments, that of the launch over the segments' states).
  *   mode 0: normal operation (the timeout_ns argument is ignored; 2 s limit).
  *
  * Process-wide setting, read at launch.  Returns KDA_OK or KDA_ERR_INVALID_ARG.

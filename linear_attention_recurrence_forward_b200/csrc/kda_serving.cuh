@@ -42,7 +42,7 @@ struct SsmArgs {
     int* status;
     unsigned long long timeout_ns;
     void* workspace;
-    int skip_handoff;          // test hook: 1 = the tensor-core kernel's first hand-off is left out
+    int skip_handoff;          // test hook: 1 = the tensor-core path's first hand-off is left out
 };
 
 cudaError_t launch_short_conv(const ConvArgs& a, cudaStream_t s);

@@ -652,7 +652,7 @@ kda_ssm_state_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
                         quarter, lane, tg);
             tmem_wait_st();
             tc_fence_before_sync();
-            warp_arrive(&bar_w[group], lane);
+            if (!(p.skip_handoff && c == 0)) warp_arrive(&bar_w[group], lane);
         }
         if (group == (chunks - 1) % ST) {
             if (ok && j == 0) {
@@ -1157,6 +1157,8 @@ cudaError_t launch_np(const CUtensorMap& mx, const CUtensorMap& mb, const CUtens
     }
     const cudaError_t e = AllowSmem<N, P, false>::once();
     if (e != cudaSuccess) return e;
+    Params last = p;
+    if (p.seg_chunks > 0) last.skip_handoff = 0;                          // the first launch has left out one
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
@@ -1167,7 +1169,7 @@ cudaError_t launch_np(const CUtensorMap& mx, const CUtensorMap& mb, const CUtens
     cfg.stream = s;
     cfg.attrs = &early;
     cfg.numAttrs = p.seg_chunks > 0 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kda_ssm_tc_kernel<N, P>, mx, mb, mc, my, p);
+    return cudaLaunchKernelEx(&cfg, kda_ssm_tc_kernel<N, P>, mx, mb, mc, my, last);
 }
 
 }  // namespace

@@ -540,3 +540,22 @@ def test_no_skip_term_adds_nothing_to_infinities(dtype, N, P):
         inf[0, 2:, 1, 7] = True
         assert torch.equal(out == float("inf"), inf) and bool(out[~inf].isfinite().all())
         assert bool((state[0, 1, :, 7] == float("inf")).all()) and int(state.isfinite().sum()) == state.numel() - N
+
+
+@gpu
+@pytest.mark.parametrize("T,H,P", [(4096, 2, 128), (1700, 1, 64)])
+def test_a_wait_that_runs_out_in_a_segment_is_reported(T, H, P):
+    """The launch over the segments' states ends by itself when one of its waits runs out (the launch after it has all
+    its hand-offs), says so, and the next call is as if nothing had been."""
+    c = case((1, T), H, 1, 128, P, "bf16", seed=8)
+    assert kda.ssm_workspace_bytes(1, T, H, 128, P) > 0
+    want = kda.kda_ssm_forward(**c)
+    kda.kda_debug_set_wait_fault(1, 20_000_000)
+    try:
+        kda.kda_ssm_forward(**c)
+        assert kda.kda_get_device_status() == STATUS["KDA_ERR_TIMEOUT"]
+    finally:
+        kda.kda_debug_set_wait_fault(0)
+    for _ in range(3):
+        y, S = kda.kda_ssm_forward(**c)
+        assert kda.kda_get_device_status() == 0 and torch.equal(y, want[0]) and torch.equal(S, want[1])
