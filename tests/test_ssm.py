@@ -559,3 +559,59 @@ def test_a_wait_that_runs_out_in_a_segment_is_reported(T, H, P):
     for _ in range(3):
         y, S = kda.kda_ssm_forward(**c)
         assert kda.kda_get_device_status() == 0 and torch.equal(y, want[0]) and torch.equal(S, want[1])
+
+
+@gpu
+@pytest.mark.parametrize("B,T,H,G,N,P", LONG + [(1, 3000, 6, 2, 128, 64)])
+def test_segments_with_what_is_optional(B, T, H, G, N, P):
+    """Prompts cut into segments without S0, without D and dt_bias, without a wanted state, from slices of wider rows.
+    The workspace starts as NaN: what is read of it was written."""
+    c = case((B, T), H, G, N, P, "bf16", seed=T + 1, rate=1.5)
+    need = kda.ssm_workspace_bytes(B, B * T, H, N, P)
+    assert need > 0
+    ws = lambda: torch.full((need,), 255, dtype=torch.uint8, device="cuda")  # noqa: E731
+    bare = {k: c[k] for k in ("x", "dt", "A", "Bm", "Cm")}
+    y, S = kda.kda_ssm_forward(**bare, workspace=ws())
+    assert kda.kda_get_device_status() == 0
+    for b in range(B):
+        check(y[b], S[b], c, b, b, "bf16", "tcgen05", skip=False, start=False)
+    y1, none = kda.kda_ssm_forward(**bare, workspace=ws(), return_state=False)
+    assert none is None and torch.equal(y, y1)
+    want, want_S = kda.kda_ssm_forward(**c)
+    y2, none = kda.kda_ssm_forward(**c, workspace=ws(), return_state=False)
+    assert none is None and torch.equal(y2, want)
+    wide = torch.full((B, T, H * P + 2 * G * N + H + 8 - H % 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    parts, at = {}, 0
+    for k, n in (("x", H * P), ("Bm", G * N), ("Cm", G * N), ("dt", H)):
+        wide[..., at:at + n] = c[k].flatten(2)
+        parts[k] = wide[..., at:at + n].unflatten(2, c[k].shape[2:])
+        at += n
+    y3, S3 = kda.kda_ssm_forward(**{**c, **parts}, workspace=ws())
+    assert torch.equal(y3, want) and torch.equal(S3, want_S)
+
+
+@gpu
+@pytest.mark.parametrize("P", [64, 128])
+@pytest.mark.parametrize("lengths,H", [([1, 130, 257, 384, 511, 640, 90, 256] * 3, 24), ([3000, 0, 129, 2500, 1500], 2)])
+def test_every_call_beside_heavy_traffic(P, lengths, H):
+    """As above, each of a thousand calls compared on the device: short packed prompts, and prompts cut into segments."""
+    T = sum(lengths)
+    c = case((T,), H, 2, 128, P, "bf16", seed=11, states=len(lengths))
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device="cuda")
+    y0, S0 = kda.kda_ssm_forward_varlen(**c, cu_seqlens=cu)
+    a, b = (torch.empty(1 << 28, dtype=torch.uint8, device="cuda") for _ in range(2))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    bad = torch.zeros((), dtype=torch.int32, device="cuda")
+    y, S = torch.empty_like(y0), torch.empty_like(S0)
+    for i in range(1000):
+        if i % 4 == 0:
+            with torch.cuda.stream(side):
+                b.copy_(a)
+        y.fill_(7.0)
+        S.fill_(7.0)
+        kda.kda_ssm_forward_varlen(**c, cu_seqlens=cu, y=y, S_T=S)
+        bad += ((y != y0).any() | (S != S0).any()).int()
+    torch.cuda.synchronize()
+    assert kda.kda_get_device_status() == 0
+    assert int(bad) == 0
