@@ -398,6 +398,10 @@ typedef enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 } kda_activation;
  *               May be `state` itself; no other overlap between outputs and inputs.
  *   W         : 2, 3 or 4.  C: a positive multiple of 8.
  *
+ * The KDA prefill takes contiguous q, k and v.  Where they are slices of one projection, a call for each
+ * slice (x with the projection's row stride, the slice's rows of weight and bias, a state of its own)
+ * leaves them contiguous without a copy.
+ *
  * T == 0 copies state to state_out.  Returns KDA_OK; KDA_ERR_UNSUPPORTED for another W, a C that is
  * not a multiple of 8, another dtype or activation; KDA_ERR_INVALID_ARG for a B or T above 2e9 too.
  */
@@ -456,9 +460,15 @@ KDA_API int kda_short_conv_step_paged(const void* x, const void* weight, const v
  *   S_T     : [B, H, N, P]  fp32 output, or NULL; may be S0 itself; no other overlap
  *   N, P    : 64 or 128.  G divides H.
  *   impl    : kda_impl.  KDA_IMPL_AUTO runs the chunked tensor-core kernel for bf16 and the
- *             token-serial fp32 kernel for fp32; KDA_IMPL_TCGEN05 refuses fp32.
+ *             token-serial fp32 kernel for fp32; KDA_IMPL_TCGEN05 refuses fp32.  KDA_IMPL_SIMT takes
+ *             bf16 too, at many times the time.
  *   workspace, workspace_bytes : DEVICE memory of at least kda_ssm_workspace(...) bytes, 16-byte
  *             aligned (NULL when that is 0), not used by anything else until the work is done.
+ *
+ * Precision.  The token-serial kernel and the single-token steps compute in fp32 throughout.  The
+ * tensor-core kernel holds S in fp32, reads it and the decayed scores C.B as bf16 operands for y (2^-8 of
+ * a term of y at most, beside the rounding of y itself), and adds to S terms that are off by 3 * 2^-16 of
+ * themselves at most.
  *
  * The tensor-core kernel forms whole 128-token blocks: a non-finite value in one token's x, B or dt
  * may reach the outputs of other tokens of its block, earlier ones too.  A NaN in A[h] makes head h's
@@ -476,6 +486,10 @@ KDA_API int kda_ssm_forward(const void* x, const void* dt, const float* A, const
  *   x, dt, Bm, Cm, y : [T_total, ...]; cu_seqlens : [n_seq + 1] int32 DEVICE array, rules of
  *                      kda_forward_varlen.  y rows outside every sequence are not written.
  *   S0, S_T          : [n_seq, H, N, P]
+ *
+ * The tensor-core kernel cuts sequences into segments that run side by side where heads and sequences are
+ * few, by the mean length T_total / n_seq (the offsets are not read on the host): one long sequence packed
+ * with many short ones is not cut, and is faster in a call of its own.
  */
 KDA_API int kda_ssm_forward_varlen(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
                                    const int* cu_seqlens, const float* D, const float* dt_bias, const float* S0,
@@ -512,7 +526,9 @@ KDA_API int kda_ssm_decode_step_paged(const void* x, const void* dt, const float
  * kda_pool -- one state pool as the pool operators see it: n_slots slots of `pieces` runs of
  * piece_bytes each.  A pool [n_slots, H, dk, dv] is one piece a slot; the boundary states of one batch
  * entry, S_mid[b] of kda_forward_chunked_states ([H, n_mid, dk, dv], slot = boundary), are H pieces.
- * All byte counts and the base are multiples of 16.
+ * All byte counts and the base are multiples of 16.  Pools are told apart by the whole range from their
+ * first to their last byte: layers that interleave in memory ([n_slots, layers, ...]) go into a call as one
+ * pool whose slots hold them all.
  */
 typedef struct {
     void* base;
@@ -543,7 +559,7 @@ KDA_API int kda_pool_copy(const kda_pool* dst, const kda_pool* src, int n_pools,
 
 /*
  * kda_pool_clear -- set slots to zero bytes in every pool: the state a new sequence starts from.
- *   idx : [n] int32 DEVICE array; negative entries are skipped, entries >= n_slots are skipped and set
+ *   idx : [n] int32 DEVICE array, n at most 2^20; negative entries are skipped, entries >= n_slots are skipped and set
  *         the status word.
  */
 KDA_API int kda_pool_clear(const kda_pool* pools, int n_pools, int n_slots, const int* idx, int n,
@@ -556,7 +572,7 @@ KDA_API int kda_pool_clear(const kda_pool* pools, int n_pools, int n_slots, cons
  * ascending order, move into the slots < L that are not live, in ascending order, in every pool; the
  * other slots keep their contents.
  *
- *   slots     : [B] int32 DEVICE array, the table of kda_decode_step_paged
+ *   slots     : [B] int32 DEVICE array, the table of kda_decode_step_paged; B at most 2^20
  *   done      : [B] bytes (0 or not) in DEVICE memory, or NULL for none ended
  *   slots_out : [B] int32 DEVICE output: the new table, -1 for sequences that are not live.  May be
  *               slots itself.

@@ -629,7 +629,10 @@ def kda_short_conv(x, weight, bias=None, state=None, *, activation="silu", y=Non
                    return_state: bool = True, stream=None):
     """The short causal convolution over x [B, T, C] (rows may be slices of wider ones): weight [C, W],
     bias [C] or None, state [B, W-1, C] (the inputs before token 0; None for zeros).  Returns (y [B, T, C],
-    state_out [B, W-1, C] or None).  state_out may be state itself.  activation: "silu" or None."""
+    state_out [B, W-1, C] or None).  state_out may be state itself.  activation: "silu" or None.
+
+    For the KDA prefill, whose q, k and v are contiguous, convolve each slice of the projection in a call of its
+    own: y comes out contiguous."""
     B, T = x.shape[:2]
     C, W, y, ldx, ldy, w, b, act = _conv_common(x, (B, T), weight, bias, y, activation, stream)
     dev, dt = x.device, x.dtype
@@ -743,7 +746,12 @@ def kda_ssm_forward(x, dt, A, Bm, Cm, D=None, dt_bias=None, S0=None, *, y=None, 
     """Prefill of the selective scan with one decay per head: x [B, T, H, P], dt [B, T, H], Bm, Cm
     [B, T, G, N] (bf16 or fp32; token rows may be slices of wider ones), A, D, dt_bias [H] fp32, S0
     [B, H, N, P] fp32.  Returns (y [B, T, H, P], S_T [B, H, N, P] or None).  S_T may be S0 itself.
-    `workspace`: a device tensor of ssm_workspace_bytes(B, B * T, ...) bytes, allocated if not given."""
+    `workspace`: a device tensor of ssm_workspace_bytes(B, B * T, ...) bytes, allocated if not given.
+
+    bf16 runs on the tensor core ("auto"): the state is held in fp32, but read for y as a bf16 operand, and its
+    new terms are off by up to 3 * 2**-16; a NaN or infinity in one token's x, B or dt may reach other tokens of
+    its 128-token block, earlier ones too.  impl="simt" computes in fp32, token by token, and takes many times as
+    long."""
     B, T = x.shape[:2]
     H, G, N, P, y, lds, d, bias = _ssm_common(x, dt, A, Bm, Cm, D, dt_bias, (B, T), y, stream)
     dev, ty = x.device, x.dtype
@@ -767,7 +775,8 @@ def kda_ssm_forward_varlen(x, dt, A, Bm, Cm, cu_seqlens, D=None, dt_bias=None, S
                            return_state: bool = True, workspace=None, impl: str = "auto", stream=None):
     """kda_ssm_forward over packed sequences: x [T_total, H, P], dt [T_total, H], Bm, Cm [T_total, G, N],
     cu_seqlens int32 [n_seq + 1] on the device, states [n_seq, H, N, P].  Returns (y [T_total, H, P], S_T or
-    None)."""
+    None).  Long sequences are cut into parts that run side by side by the mean length: one long sequence among
+    many short ones is faster in a call of its own."""
     T_total = x.shape[0]
     n_seq = cu_seqlens.shape[0] - 1
     H, G, N, P, y, lds, d, bias = _ssm_common(x, dt, A, Bm, Cm, D, dt_bias, (T_total,), y, stream)

@@ -24,9 +24,11 @@
 //
 // What bounds it.  Per chunk of a 128-column tile HBM moves 64 KB of x and y (2.8K cycles at the measured
 // copy rate with all SMs at it), the tensor core needs 2.5K cycles, and shared memory 3.5K (the products'
-// operands and the tiles' own way in and out).  A chunk takes about 4.9K (4 x 8192 tokens, 96 heads of 128:
-// 530 us, 3.0 TB/s of x and y; more with a cold L2), 4.2K where nothing contends.  Loops of about one length
-// bound it: the warps' own steps, each a pass from tensor memory through registers and back; C S, the
+// operands and the tiles' own way in and out).  4 x 8192 tokens with 96 heads of 128, three waves of 64
+// chunks, take 527 to 535 us for the first 50 ms of a run, at 1965 MHz: 5.4K cycles a chunk, 4.2K where nothing
+// contends.  Kept up for seconds the GPU reaches its power limit and about 1.5 GHz, and they take 610 to 636 us:
+// 4.8K of the longer cycles, of which HBM takes fewer.  (Times of variants below are of short runs.)  Loops of
+// about one length bound it: the warps' own steps, each a pass from tensor memory through registers and back; C S, the
 // update, the weighted x and the carried state, which wait for one another; and the loads of B and C.
 // Operands are kept out of shared memory where a product allows: Q and the weighted x are tensor-memory
 // operands, and the state is held transposed (lanes = value columns) for that.  The weighted x is transposed

@@ -292,3 +292,22 @@ def test_fp32_activation_to_the_last_places(step):
     assert np.all(err <= 10 * 2.0 ** -24 * np.abs(ref_y) + 2.0 ** -147 * (1 + np.abs(z))), float((err / np.abs(ref_y + 1e-300)).max())
     assert bool(torch.isnan(kda.kda_short_conv(torch.full((1, 1, 8), float("nan"), device="cuda"), w)[0]).all())
     assert bool((kda.kda_short_conv(torch.full((1, 1, 8), float("inf"), device="cuda"), w)[0] == float("inf")).all())
+
+
+@gpu
+def test_slices_of_a_projection_feed_the_prefill_without_copies():
+    """A call for each of q, k and v, slices of one projection: contiguous outputs that the KDA prefill takes as they
+    are, equal to those of one call over all three, and states that carry the prompt on."""
+    B, T, H, d = 2, 130, 2, 64
+    C = H * d
+    proj, w = rand((B, T, 3 * C), "bf16", 1), rand((3 * C, 4), "bf16", 2, 0.5)
+    g, beta = -rand((B, T, H, d), "bf16", 3).abs(), rand((B, T, H), "bf16", 4).sigmoid()
+    whole, end = kda.kda_short_conv(proj, w)
+    parts = [kda.kda_short_conv(proj[..., i * C:(i + 1) * C], w[i * C:(i + 1) * C]) for i in range(3)]
+    for i, (y, st) in enumerate(parts):
+        assert y.is_contiguous() and torch.equal(y, whole[..., i * C:(i + 1) * C])
+        assert torch.equal(st, end[..., i * C:(i + 1) * C])
+    q, k, v = (y.view(B, T, H, d) for y, _ in parts)
+    q, k = (torch.nn.functional.normalize(t.float(), dim=-1).bfloat16() for t in (q, k))
+    o, S = kda.kda_forward_chunked(q, k, v, g, beta)
+    assert kda.kda_get_device_status() == 0 and bool(o.isfinite().all()) and bool(S.isfinite().all())
