@@ -68,4 +68,18 @@ int wait_fault_mode();     // kda_debug_set_wait_fault
 // softplus(v) = log(1 + e^v) without overflow or cancellation
 __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
 
+// A token's decay e^v, v = step * A.  A state that remembers thousands of tokens is multiplied by thousands of decays just
+// below 1, so that what expf is off by there, on one side, adds up (1.3e-8 a token: 1.3e-5 of a state that remembers a
+// thousand).  Near 0 it is the power series, 1 + v + .. + v^6 / 720 (what is left out is below 2^-26), whose one rounding
+// that counts is the last, to nearest: 1.0e-6 of that state.  Further from 0 a state forgets within a few tokens.
+__device__ __forceinline__ float token_decay(float v) {
+    float near = fmaf(v, 1.f / 720.f, 1.f / 120.f);
+    near = fmaf(v, near, 1.f / 24.f);
+    near = fmaf(v, near, 1.f / 6.f);
+    near = fmaf(v, near, 0.5f);
+    near = fmaf(v, near, 1.f);
+    near = fmaf(v, near, 1.f);
+    return fabsf(v) < 0.25f ? near : expf(v);
+}
+
 }  // namespace kda

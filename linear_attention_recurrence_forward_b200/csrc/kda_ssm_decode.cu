@@ -66,7 +66,7 @@ kda_ssm_decode_kernel(const T* __restrict__ x, const T* __restrict__ dt, const f
     if (tid < N) bs[tid] = load_elem(Bm, b * ldb + (size_t)g * N + tid);
     else if (tid - 128 >= 0 && tid - 128 < N) cs[tid - 128] = load_elem(Cm, b * ldc + (size_t)g * N + (tid - 128));
     const float step = softplus(load_elem(dt, b * lddt + h) + (dt_bias ? dt_bias[h] : 0.f));
-    const float a = expf(step * A[h]);
+    const float a = token_decay(step * A[h]);
     const float4 xv = load4(x + b * ldx + (size_t)h * P + col);
     const float4 u = make_float4(step * xv.x, step * xv.y, step * xv.z, step * xv.w);
     __syncthreads();

@@ -92,7 +92,7 @@ kda_ssm_simt_kernel(const T* __restrict__ x, const T* __restrict__ dt, const flo
     auto stage_dt = [&](float v, int t0, int buf) {
         if (tid < kTok && t0 + tid < len) {
             const float st = softplus(v + bias);
-            as[buf][tid] = make_float2(expf(st * rate), st);
+            as[buf][tid] = make_float2(token_decay(st * rate), st);
         }
     };
 
