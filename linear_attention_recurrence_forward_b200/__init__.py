@@ -748,8 +748,9 @@ def kda_ssm_forward(x, dt, A, Bm, Cm, D=None, dt_bias=None, S0=None, *, y=None, 
     [B, H, N, P] fp32.  Returns (y [B, T, H, P], S_T [B, H, N, P] or None).  S_T may be S0 itself.
     `workspace`: a device tensor of ssm_workspace_bytes(B, B * T, ...) bytes, allocated if not given.
 
-    bf16 runs on the tensor core ("auto"): the state is held in fp32, but read for y as a bf16 operand, and its
-    new terms are off by up to 3 * 2**-16; a NaN or infinity in one token's x, B or dt may reach other tokens of
+    bf16 runs on the tensor core ("auto"): the state is held in fp32, but read for y as a bf16 operand, its new
+    terms are off by up to 3 * 2**-16, and it loses up to 16 * 2**-23 of itself for each 128 tokens that it
+    remembers; a NaN or infinity in one token's x, B or dt may reach other tokens of
     its 128-token block, earlier ones too.  impl="simt" computes in fp32, token by token, and takes many times as
     long."""
     B, T = x.shape[:2]

@@ -643,3 +643,19 @@ def test_a_long_memory_does_not_drift(N, P):
     for t in range(T):
         kda.kda_ssm_decode_step(c["x"][:, t], c["dt"][:, t], c["A"], c["Bm"][:, t], c["Cm"][:, t], held, c["D"], c["dt_bias"])
     assert drift(held[0]) <= 2.3e-6
+
+
+@gpu
+@pytest.mark.parametrize("B,H,P", [(4, 96, 64), (1, 2, 64), (1, 2, 128)])
+def test_a_long_memory_of_the_tensor_core(B, H, P):
+    """Without decay and from positive inputs the tensor core's sums lose at most 16 * 2^-23 of the state a chunk, the
+    weights and weighted x at most 3 * 2^-16 of a term: in one run of chunks, and cut into segments."""
+    T, N = 4096, 128
+    c = case((B, T), H, 1, N, P, "bf16", seed=13)
+    for k in ("x", "Bm", "S0"):
+        c[k] = c[k].abs()
+    c["A"].zero_()
+    _, S = kda.kda_ssm_forward(**c, impl="tcgen05")
+    step = torch.logaddexp(c["dt"][0, :, :2].double() + c["dt_bias"][:2].double(), torch.zeros((), dtype=torch.float64, device="cuda"))
+    want = torch.einsum("tn,th,thp->hnp", c["Bm"][0, :, 0].double(), step, c["x"][0, :, :2].double()) + c["S0"][0, :2].double()
+    assert bool(((S[0, :2].double() - want).abs() <= (T // 128 * 16 * 2.0 ** -23 + 3 * 2.0 ** -16 + 2.0 ** -20) * want).all())
