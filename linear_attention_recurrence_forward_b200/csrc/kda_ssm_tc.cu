@@ -22,8 +22,9 @@
 // hi = x w1 rounded and lo = x w2 + (x w1 - hi) rounded (x w1 - hi is exact), so a term of the state is
 // off by at most 3 * 2^-16 of itself.  The sixteen products of a chunk that add to the state round it towards
 // zero, up to 2^-23 of it each (8e-7 a chunk measured: 3.9e-5 after 8192 tokens without decay, 6e-6 of a state
-// that remembers a thousand tokens).  To keep the state's leading bits out of those sums (its bf16 copy lies in
-// shared memory) would take some 130 instructions a thread and chunk on top of 640.
+// that remembers a thousand tokens).  With the state's leading bits kept out of those sums (the carried state less
+// its bf16 copy, which lies in shared memory, added again a chunk later) 3.3e-7 of it were lost at any length, but
+// the launches took 7 to 9 % longer (621 -> 679 us); the outputs' own rounding, 2^-8, hides either.
 //
 // What bounds it.  Per chunk of a 128-column tile HBM moves 64 KB of x and y (2.8K cycles at the measured
 // copy rate with all SMs at it), the tensor core needs 2.5K cycles, and shared memory 3.5K (the products'
