@@ -465,12 +465,13 @@ KDA_API int kda_short_conv_step_paged(const void* x, const void* weight, const v
  *   workspace, workspace_bytes : DEVICE memory of at least kda_ssm_workspace(...) bytes, 16-byte
  *             aligned (NULL when that is 0), not used by anything else until the work is done.
  *
- * Precision.  The token-serial kernel and the single-token steps compute in fp32 throughout.  The
- * tensor-core kernel holds S in fp32, reads it and the decayed scores C.B as bf16 operands for y (2^-8 of
- * a term of y at most, beside the rounding of y itself), and adds to S terms that are off by 3 * 2^-16 of
- * themselves at most.  The tensor core's sums are rounded towards zero, 16 times for a chunk of 128 tokens: S
- * loses up to 16 * 2^-23 of itself for each chunk that it remembers (about 8e-7: 6e-6 of a state that
- * remembers a thousand tokens, 4e-4 after 65536 tokens without any decay).
+ * Precision.  The token-serial kernel and the single-token steps compute in fp32 throughout; a token's
+ * decay is one fp32 number, off by up to 2^-25 of the state where it is near 1.  The tensor-core kernel
+ * holds S in fp32, reads it and the decayed scores C.B as bf16 operands for y (2^-8 of a term of y at most,
+ * beside the rounding of y itself), and adds to S terms that are off by 3 * 2^-16 of themselves at most.
+ * The tensor core's sums are rounded towards zero, 16 times for a chunk of 128 tokens: S loses up to
+ * 16 * 2^-23 of itself for each chunk that it remembers (about 8e-7: 6e-6 of a state that remembers a
+ * thousand tokens, 4e-4 after 65536 tokens without any decay).
  *
  * The tensor-core kernel forms whole 128-token blocks: a non-finite value in one token's x, B or dt
  * may reach the outputs of other tokens of its block, earlier ones too.  A NaN in A[h] makes head h's
