@@ -7,7 +7,7 @@
 // registers between the read and the write.  There is no residual here, so the new state does not
 // wait for any reduction: it is stored as soon as it is formed, and the column sums S^T C follow
 // through warp shuffles and one shared-memory step.  One B200, 256 sequences x 96 heads of 128 x 128,
-// bf16: 478 us for 3.2 GB, 1.03 of the measured copy rate (an update in place: the same lines go back).
+// bf16: 481 us for 3.2 GB, 1.03 of the measured copy rate (an update in place: the same lines go back).
 #include "kda_serving.cuh"
 
 namespace kda {
@@ -58,16 +58,19 @@ kda_ssm_decode_kernel(const T* __restrict__ x, const T* __restrict__ dt, const f
         }
         at = (size_t)sl * H + h;
     }
+    // everything else is asked for before the state, whose loads are many: what its update waits for comes first (481 us;
+    // in the other order 490)
+    const float raw = load_elem(dt, b * lddt + h), bias = dt_bias ? dt_bias[h] : 0.f, rate = A[h], skip = D ? D[h] : 0.f;
+    const int g = h / rep;
+    if (tid < N) bs[tid] = load_elem(Bm, b * ldb + (size_t)g * N + tid);
+    else if (tid - 128 >= 0 && tid - 128 < N) cs[tid - 128] = load_elem(Cm, b * ldc + (size_t)g * N + (tid - 128));
+    const float4 xv = load4(x + b * ldx + (size_t)h * P + col);
     float4* Sv = reinterpret_cast<float4*>(S + at * N * P + col);
     float4 s[RPT];
 #pragma unroll
     for (int j = 0; j < RPT; ++j) s[j] = __ldcs(Sv + (size_t)(rg + j * kRpp) * (P / 4));
-    const int g = h / rep;
-    if (tid < N) bs[tid] = load_elem(Bm, b * ldb + (size_t)g * N + tid);
-    else if (tid - 128 >= 0 && tid - 128 < N) cs[tid - 128] = load_elem(Cm, b * ldc + (size_t)g * N + (tid - 128));
-    const float step = softplus(load_elem(dt, b * lddt + h) + (dt_bias ? dt_bias[h] : 0.f));
-    const float a = token_decay(step * A[h]);
-    const float4 xv = load4(x + b * ldx + (size_t)h * P + col);
+    const float step = softplus(raw + bias);
+    const float a = token_decay(step * rate);
     const float4 u = make_float4(step * xv.x, step * xv.y, step * xv.z, step * xv.w);
     __syncthreads();
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -94,8 +97,8 @@ kda_ssm_decode_kernel(const T* __restrict__ x, const T* __restrict__ dt, const f
             o.x += t.x; o.y += t.y; o.z += t.z; o.w += t.w;
         }
         if (D) {                              // this thread's columns: tid == c4
-            const float d = D[h];
-            o.x = fmaf(d, xv.x, o.x); o.y = fmaf(d, xv.y, o.y); o.z = fmaf(d, xv.z, o.z); o.w = fmaf(d, xv.w, o.w);
+            o.x = fmaf(skip, xv.x, o.x); o.y = fmaf(skip, xv.y, o.y);
+            o.z = fmaf(skip, xv.z, o.z); o.w = fmaf(skip, xv.w, o.w);
         }
         store4(y + bh * P + col, o);
     }
